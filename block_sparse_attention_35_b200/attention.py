@@ -12,12 +12,25 @@ applies PBSA with top-k and updates P and L):
                                          # means the key-mean cache; sink frames their slots
     out = attn(q_chunk, accumulate_mass=True)   # select + forward (+ block mass)
     attn.slide()                         # evict old frames, merge them into P
+
+Queries and keys that come straight from their projections go through attn.norm_rope first
+(RMS norm of every head, rotation by frame, row and column), and their gradients through
+attn.norm_rope_backward.
 """
 from __future__ import annotations
 
 import torch
 
 from . import pbsa as P
+
+
+def rope_table(axis_pairs, length: int, theta: float = 10000.0, device="cuda"):
+    """(cos, sin) [length, sum(axis_pairs)] fp32 for pbsa_qk_norm_rope: pair j of an axis with n
+    pairs turns by position * theta^(-j / n).  The angles are formed in 64 bits, where far
+    positions keep their fraction of a turn."""
+    inv = torch.cat([theta ** (-torch.arange(n, dtype=torch.float64) / max(n, 1)) for n in axis_pairs])
+    ang = torch.arange(length, dtype=torch.float64)[:, None] * inv
+    return ang.cos().float().to(device), ang.sin().float().to(device)
 
 
 class SparseForcingAttention:
@@ -82,6 +95,8 @@ class SparseForcingAttention:
         self.ws_fwd = torch.empty(max(1, P.pbsa_workspace_size(self.cfg, P.PBSA_OP_FWD, qf)), **u8)
         self.ws_bwd = torch.empty(max(1, P.pbsa_workspace_size(self.cfg, P.PBSA_OP_BWD, qf)), **u8)
         self._grads = None
+        self._heads = {}              # by frames of the call: see norm_rope
+        self._rope = None
 
     # ------------------------------------------------------------------ cache plumbing
     def ring_slot(self, p: int) -> int:
@@ -130,6 +145,57 @@ class SparseForcingAttention:
             self.pers_score.copy_(pers_score)
         if pers_src is not None:
             self.pers_src.copy_(pers_src)
+
+    # ------------------------------------------------------- heads: norm and rotation
+    def _heads_of(self, n_frames: int, grad_dtype):
+        """Configuration and position buffer of norm_rope calls over n_frames frames."""
+        key = (n_frames, grad_dtype)
+        if key not in self._heads:
+            p = self.D // 2
+            pairs = (p - 2 * (p // 3), p // 3, p // 3)     # frame, row, column
+            fh, fw = self.cfg.frame_h, self.cfg.frame_w
+            length = max(self.cfg.max_seq_len // self.tf, fh, fw)
+            if self._rope is None:
+                self._rope = rope_table(pairs, length, device=self.device)
+            cfg = P.make_qk_config(self.B, n_frames * self.tf, self.H, self.H, self.D,
+                                   interleaved=True, axis_pairs=pairs, table_len=length,
+                                   grad_dtype=grad_dtype)
+            t = torch.arange(n_frames * self.tf, device=self.device)
+            pos = torch.stack((t // self.tf, t % self.tf // fw, t % fw), -1).int()
+            pos = pos.expand(self.B, -1, -1).contiguous()
+            ws = torch.empty(P.pbsa_qk_workspace_size(cfg), dtype=torch.uint8, device=self.device)
+            self._heads[key] = cfg, pos, ws
+        return self._heads[key]
+
+    def _head_positions(self, pos, first_frame: int):
+        if first_frame == 0:
+            return pos
+        return pos + torch.tensor([first_frame, 0, 0], dtype=torch.int32).to(self.device)
+
+    def norm_rope(self, q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, first_frame: int):
+        """RMS-normalises every head of the projected queries and keys [B, frames*T_f, H, D]
+        (views of one projection's output will do), scales it by its weight ([D] fp32 or None)
+        and rotates it by its token's frame (first_frame, first_frame + 1, ... of the sequence,
+        below max_seq_len / T_f), row and column.  Returns new (q, k), ready for append() and
+        the call."""
+        cfg, pos, _ = self._heads_of(q.shape[1] // self.tf, torch.bfloat16)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        P.pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, *self._rope,
+                            self._head_positions(pos, first_frame), q_out, k_out, self.status)
+        return q_out, k_out
+
+    def norm_rope_backward(self, q, k, q_weight, k_weight, first_frame: int, dq_out, dk_out):
+        """Gradients of norm_rope from those of its outputs (bf16, or fp32 as backward() gives
+        them).  Returns (dq, dk, dq_weight, dk_weight); a weight that is None has no gradient."""
+        cfg, pos, ws = self._heads_of(q.shape[1] // self.tf, dq_out.dtype)
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dw = [None if w is None else torch.empty_like(w) for w in (q_weight, k_weight)]
+        P.pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, *self._rope,
+                                self._head_positions(pos, first_frame), dq_out, dk_out, dq, dk,
+                                dw[0], dw[1], ws, self.status)
+        return dq, dk, dw[0], dw[1]
 
     # ------------------------------------------------------------------ the method
     def select(self, q: torch.Tensor, q_frames: int | None = None):

@@ -1,0 +1,162 @@
+// kv4_append.cu - new tokens into the 4-bit token cache, and its rows back as values.
+//
+// Format (include/pbsa.h): sixteen channels share scale = e4m3(amax / 6 / unit); a channel is
+// the e2m1 code nearest to x / unit / scale.
+//
+// Every rounding is the format's own: inputs have at most 11 significant bits and the borders
+// between codes (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5 times an e4m3 scale) at most 7, so an
+// input that is not on a border is at least 2^-11 of it away, far more than the half ulp of the
+// IEEE division below, and one that is on it divides exactly: the code is that of exact
+// arithmetic, ties included.  The same holds for amax / 6 against the borders of e4m3.
+//
+// append_kernel and read_kernel are bound by HBM: one thread owns one block of sixteen
+// channels, 32 bytes of a 16-bit type against 8 bytes of codes and one scale byte; neighbouring
+// threads own neighbouring blocks, so a warp touches whole sectors on both sides.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv4_device.cuh"
+#include "pbsa_device.cuh"
+#include "token_internal.cuh"
+
+namespace pbsa {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float2 widen2(uint32_t u, __nv_bfloat16*) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 widen2(uint32_t u, __half*) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, __nv_bfloat16*) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, __half*) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Quantises sixteen values (already divided by the unit): 8 bytes of codes and the scale byte.
+__device__ __forceinline__ uint2 quantise16(const float (&x)[16], uint8_t* scale) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    const uint8_t sb = e4m3_from_float(__fdiv_rn(amax, 6.f));
+    *scale = sb;
+    const float s = e4m3_to_float(sb);
+    uint32_t w[2] = {0, 0};
+    if (s > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i / 4] |= e2m1x2_from_float(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i % 4));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_kernel(Kv4Args a, float inv_unit_k, float inv_unit_v) {
+    const pbsa_kv4_config& c = a.c;
+    const int gpr = c.D / 16;   // blocks of a row
+    // thread -> (sequence, token, key head, keys or values, block): the source's order
+    long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int g = (int)(i % gpr);
+    i /= gpr;
+    const int h = (int)(i % c.Hkv);
+    i /= c.Hkv;
+    const int t = (int)(i % a.T);
+    i /= a.T;
+    const int b = (int)(i % c.B);
+    const int is_v = (int)(i / c.B);
+    if (is_v > 1) return;
+    const int pos = a.pos_new[(size_t)b * a.T + t];
+    if (pos < 0) return;
+    const size_t bh = (size_t)b * c.Hkv + h;
+    const int row = a.rows ? a.rows[bh * a.T + t] : pos;
+    if (row < 0 || row >= c.capacity) {
+        set_status(a.status, PBSA_ERR_DEVICE_CHECK);
+        return;
+    }
+    const Strides& s = is_v ? a.sv : a.sk;
+    const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) + b * s.b + t * s.t + h * s.h + 16 * g;
+    const uint4 lo = reinterpret_cast<const uint4*>(src)[0], hi = reinterpret_cast<const uint4*>(src)[1];
+    const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const float inv = is_v ? inv_unit_v : inv_unit_k;
+    float x[16];
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 v = widen2(u[j], static_cast<T*>(nullptr));
+        nan |= (v.x != v.x) || (v.y != v.y);
+        x[2 * j] = v.x == v.x ? v.x * inv : 0.f;
+        x[2 * j + 1] = v.y == v.y ? v.y * inv : 0.f;
+    }
+    if (nan) set_status(a.status, PBSA_ERR_DEVICE_CHECK);
+    const size_t at = (bh * c.capacity + row) * gpr + g;
+    uint8_t scale;
+    const uint2 codes = quantise16(x, &scale);
+    reinterpret_cast<uint2*>(is_v ? a.cache.v_codes : a.cache.k_codes)[at] = codes;
+    (is_v ? a.cache.v_scales : a.cache.k_scales)[at] = scale;
+    if (g == 0 && !is_v) {
+        a.cache.pos[bh * c.capacity + row] = pos;
+        if (a.mass) a.mass[bh * c.capacity + row] = 0.f;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) read_kernel(Kv4Args a) {
+    const pbsa_kv4_config& c = a.c;
+    const int gpr = c.D / 16;
+    long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int g = (int)(i % gpr);
+    i /= gpr;
+    const int j = (int)(i % a.n);
+    i /= a.n;
+    const long long bh = i % ((long long)c.B * c.Hkv);
+    const int is_v = (int)(i / ((long long)c.B * c.Hkv));
+    if (is_v > 1) return;
+    const int row = a.rows ? a.rows[(size_t)bh * a.n + j] : j;
+    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (row >= 0 && row < c.capacity) {
+        const size_t at = ((size_t)bh * c.capacity + row) * gpr + g;
+        const uint2 w = reinterpret_cast<const uint2*>(is_v ? a.cache.v_codes : a.cache.k_codes)[at];
+        const float s = e4m3_to_float((is_v ? a.cache.v_scales : a.cache.k_scales)[at]) * (is_v ? c.v_unit : c.k_unit);
+        uint32_t h[8];
+        e2m1x8_to_half2x4(w.x, h[0], h[1], h[2], h[3]);
+        e2m1x8_to_half2x4(w.y, h[4], h[5], h[6], h[7]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+            out[k] = narrow2(v.x * s, v.y * s, static_cast<T*>(nullptr));
+        }
+    } else if (row != -1) {
+        set_status(a.status, PBSA_ERR_DEVICE_CHECK);
+    }
+    T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + (((size_t)bh * a.n + j) * gpr + g) * 16;
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st) {
+    const long long n = 2ll * a.c.B * a.T * a.c.Hkv * (a.c.D / 16);
+    const unsigned blocks = (unsigned)((n + kThreads - 1) / kThreads);
+    const float ik = 1.f / a.c.k_unit, iv = 1.f / a.c.v_unit;   // exact: powers of two
+    if (a.c.dtype == PBSA_DTYPE_BF16) append_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a, ik, iv);
+    else append_kernel<__half><<<blocks, kThreads, 0, st>>>(a, ik, iv);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t st) {
+    const long long n = 2ll * a.c.B * a.n * a.c.Hkv * (a.c.D / 16);
+    const unsigned blocks = (unsigned)((n + kThreads - 1) / kThreads);
+    if (a.c.dtype == PBSA_DTYPE_BF16) read_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a);
+    else read_kernel<__half><<<blocks, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace pbsa

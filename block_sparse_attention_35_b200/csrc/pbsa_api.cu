@@ -613,6 +613,16 @@ namespace pbsa {
 
 int api_fail(int code, const char* msg) { return fail(code, "%s", msg); }
 
+int api_failf(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return code;
+}
+
 int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
 // Checks the arguments of a block selection call exactly as pbsa_select_blocks does and

@@ -148,6 +148,7 @@ cudaError_t launch_wait_selftest(int32_t* status, long long timeout_ns, cudaStre
 namespace pbsa {
 // Shared argument handling for entry points outside pbsa_api.cu.
 int api_fail(int code, const char* msg);
+int api_failf(int code, const char* fmt, ...);
 int api_cuda_fail(cudaError_t e, const char* what);
 int api_prepare_select(const pbsa_config* cfg, const void* q, int q_frames, const void* k_local,
                        int local_frames, int ring_head, const int32_t* idx, int idx_stride,

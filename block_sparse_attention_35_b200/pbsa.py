@@ -27,6 +27,10 @@ PBSA_ERR_DEVICE_CHECK = -5
 PBSA_ERR_WORKSPACE = -6
 PBSA_OP_SELECT, PBSA_OP_FWD, PBSA_OP_BWD, PBSA_OP_UPDATE = 0, 1, 2, 3
 PBSA_KV_CACHE_SPARSE_FORCING, PBSA_KV_CACHE_DENSE = 0, 1
+PBSA_DTYPE_BF16, PBSA_DTYPE_FP16, PBSA_DTYPE_FP32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: PBSA_DTYPE_BF16, torch.float16: PBSA_DTYPE_FP16,
+           torch.float32: PBSA_DTYPE_FP32}
+_TORCH = {v: k for k, v in _DTYPES.items()}
 
 
 class PBSAError(RuntimeError):
@@ -47,6 +51,74 @@ class pbsa_config(ctypes.Structure):
         ("local_block_sparse_topk_ratio", ctypes.c_float),
         ("sink_frames", ctypes.c_int),
     ]
+
+
+class pbsa_qk_config(ctypes.Structure):
+    """Mirror of the C struct pbsa_qk_config."""
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+        ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+        ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+        ("axis_pairs", ctypes.c_int * 3), ("table_len", ctypes.c_int), ("eps", ctypes.c_float),
+    ]
+
+
+class pbsa_kv4_config(ctypes.Structure):
+    """Mirror of the C struct pbsa_kv4_config."""
+    _fields_ = [
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("capacity", ctypes.c_int), ("dtype", ctypes.c_int), ("k_unit", ctypes.c_float),
+        ("v_unit", ctypes.c_float),
+    ]
+
+
+class pbsa_kv4_cache(ctypes.Structure):
+    """Mirror of the C struct pbsa_kv4_cache (make_kv4_cache fills it from tensors)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p)]
+
+
+def _dtype(dt):
+    if dt not in _DTYPES:
+        raise PBSAError(PBSA_ERR_UNSUPPORTED, f"dtype {dt}")
+    return _DTYPES[dt]
+
+
+def make_qk_config(B, T, Hq, Hkv, D, dtype=torch.bfloat16, rot_dim=None, interleaved=False,
+                   axis_pairs=None, table_len=0, eps=1e-6, grad_dtype=None) -> pbsa_qk_config:
+    """rot_dim None rotates every channel; axis_pairs None is one position component."""
+    rot_dim = D if rot_dim is None else rot_dim
+    pairs = (rot_dim // 2,) if axis_pairs is None else tuple(axis_pairs)
+    if not 1 <= len(pairs) <= 3:
+        raise PBSAError(PBSA_ERR_ARG, f"axis_pairs has {len(pairs)} entries, not 1 to 3")
+    return pbsa_qk_config(B, T, Hq, Hkv, D, _dtype(dtype),
+                          _dtype(dtype if grad_dtype is None else grad_dtype), rot_dim,
+                          int(bool(interleaved)), len(pairs),
+                          (ctypes.c_int * 3)(*pairs, *(0,) * (3 - len(pairs))), table_len,
+                          float(eps))
+
+
+def make_kv4_config(B, Hq, Hkv, D, capacity, dtype=torch.bfloat16, k_unit=1.0,
+                    v_unit=1.0) -> pbsa_kv4_config:
+    return pbsa_kv4_config(B, Hq, Hkv, D, capacity, _dtype(dtype), float(k_unit), float(v_unit))
+
+
+def make_kv4_cache(cfg, k_codes, k_scales, v_codes, v_scales, pos) -> pbsa_kv4_cache:
+    """The cache handle of its five device tensors (which it keeps alive)."""
+    pbsa_validate_kv4_config(cfg)
+    rows = (cfg.B, cfg.Hkv, cfg.capacity)
+    dev = pos.device
+    for name, t, w in (("k_codes", k_codes, cfg.D // 2), ("k_scales", k_scales, cfg.D // 16),
+                       ("v_codes", v_codes, cfg.D // 2), ("v_scales", v_scales, cfg.D // 16)):
+        _want(t, name, (*rows, w), torch.uint8, dev)
+    _want(pos, "pos", rows, torch.int32, dev)
+    c = pbsa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                       v_scales.data_ptr(), pos.data_ptr())
+    c.tensors = (k_codes, k_scales, v_codes, v_scales, pos)
+    c.device = dev
+    c.shape = (cfg.B, cfg.Hkv, cfg.capacity, cfg.D)
+    return c
 
 
 def make_config(B, H, D, frame_h, frame_w, total_cache_size, local_cache_size,
@@ -73,6 +145,9 @@ def _load():
     P = ctypes.c_void_p
     I = ctypes.c_int
     C = ctypes.POINTER(pbsa_config)
+    Z = ctypes.c_size_t
+    S = ctypes.POINTER(ctypes.c_int64)
+    QC, KC, KK = (ctypes.POINTER(t) for t in (pbsa_qk_config, pbsa_kv4_config, pbsa_kv4_cache))
     sig = {
         "pbsa_validate_config": (I, [C]),
         "pbsa_blocks_per_frame": (I, [C]),
@@ -94,6 +169,15 @@ def _load():
         "pbsa_pool_keys": (I, [C, P, I, I, P, P]),
         "pbsa_append_frames": (I, [C, P, P, I, I, P, P, I, P, P, P, P, P, P, P]),
         "pbsa_select_blocks_pooled": (I, [C, P, I, P, I, I, P, I, P, P, P, ctypes.c_size_t, P]),
+        "pbsa_qk_workspace_size": (Z, [QC]),
+        "pbsa_qk_norm_rope": (I, [QC, P, P, S, P, P, P, P, P, P, P, P, P]),
+        "pbsa_qk_norm_rope_bwd": (I, [QC, P, P, S, P, P, P, P, P, P, P, P, P, P, P, P, Z, P, P]),
+        "pbsa_validate_kv4_config": (I, [KC]),
+        "pbsa_kv4_workspace_size": (Z, [KC, I]),
+        "pbsa_kv4_append": (I, [KC, KK, P, P, S, I, P, P, P, P, P]),
+        "pbsa_kv4_read": (I, [KC, KK, P, I, P, P, P, P]),
+        "pbsa_kv4_attn": (I, [KC, KK, P, S, I, P, P, P, P, P, P, Z, P, P]),
+        "pbsa_kv4_evict": (I, [KC, P, P, I, I, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -265,3 +349,202 @@ def pbsa_select_blocks_noalloc(cfg, q, q_frames, k_local, local_frames, ring_hea
         f.argtypes = [ctypes.POINTER(pbsa_config), P, I, P, I, I, P, I, P, P, P]
     _check(f(_cfg(cfg), _ptr(q), q_frames, _ptr(k_local), local_frames, ring_head, _ptr(idx),
              idx_stride, _ptr(cnt), _ptr(scores), _stream(stream)))
+
+
+# --------------------------------------------- token operators: heads and the 4-bit cache
+# These calls check what a pointer cannot show - shapes, types, the device - before they hand
+# the pointers on, and run on the current stream of the tensors' device.
+
+def _bad(msg):
+    raise PBSAError(PBSA_ERR_ARG, msg)
+
+
+def _want(t, name, shape, dtype, device, strided=False):
+    """Checks a tensor: contiguous, or (strided) only its last dimension contiguous."""
+    if t.shape != shape:
+        _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        _bad(f"{name}: {t.dtype}, expected {dtype}")
+    if t.device != device:
+        _bad(f"{name} is on {t.device}, not on {device}")
+    if strided:
+        if t.stride(-1) != 1:
+            _bad(f"{name}: channels are not contiguous")
+    elif not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+
+
+def _strides(*tensors):
+    """Batch, token and head strides of [B, T, H, D] tensors; NULL when all are contiguous."""
+    if all(t is None or t.is_contiguous() for t in tensors):
+        return None
+    out = (ctypes.c_int64 * (3 * len(tensors)))()
+    for i, t in enumerate(tensors):
+        if t is not None:
+            out[3 * i:3 * i + 3] = t.stride()[:3]
+    return out
+
+
+def _launch(device, stream, call):
+    """Runs call(stream) with the tensors' device current; its own stream unless one is given."""
+    if device.type != "cuda":
+        _bad(f"tensors are on {device}, not on a CUDA device")
+    if torch.cuda.current_device() == device.index:
+        _check(call(_stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(stream)))
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _want_workspace(t, device):
+    if t is not None and (t.device != device or not t.is_contiguous()):
+        _bad(f"workspace is not a contiguous tensor on {device}")
+
+
+def _qk_check(cfg, tensors, q_weight, k_weight, cos, sin, pos, status):
+    """tensors: (name, query tensor, key tensor, dtype) of [B, T, H, D] pairs."""
+    dev = tensors[0][1].device
+    for name, tq, tk, dt in tensors:
+        _want(tq, "q" + name if name[:1] == "_" or not name else name + "q",
+              (cfg.B, cfg.T, cfg.Hq, cfg.D), dt, dev, True)
+        if cfg.Hkv:
+            _want(tk, "k" + name if name[:1] == "_" or not name else name + "k",
+                  (cfg.B, cfg.T, cfg.Hkv, cfg.D), dt, dev, True)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _want(w, name, (cfg.D,), torch.float32, dev)
+    if cfg.rot_dim:
+        if cos is None or sin is None or pos is None or status is None:
+            _bad("cos, sin, pos and status are needed for a rotation")
+        table = (cfg.table_len, cfg.rot_dim // 2)
+        _want(cos, "cos", table, torch.float32, dev)
+        _want(sin, "sin", table, torch.float32, dev)
+        _want(pos, "pos", (cfg.B, cfg.T, cfg.n_axes), torch.int32, dev)
+    if status is not None:
+        _want(status, "status", (1,), torch.int32, dev)
+    return dev
+
+
+def pbsa_qk_workspace_size(cfg) -> int:
+    n = _lib.pbsa_qk_workspace_size(_cfg(cfg))
+    if n == 0:
+        raise PBSAError(PBSA_ERR_ARG, pbsa_last_error())
+    return n
+
+
+def pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, pos, q_out, k_out, status,
+                      stream=None):
+    """RMS norm and rotation of every head; q, k, q_out, k_out may be strided views."""
+    dt = _TORCH.get(cfg.dtype)
+    if not cfg.Hkv:
+        k = k_out = None
+    dev = _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos,
+                    sin, pos, status)
+    _launch(dev, stream, lambda s: _lib.pbsa_qk_norm_rope(
+        _cfg(cfg), _ptr(q), _ptr(k), _strides(q, k, q_out, k_out), _ptr(q_weight),
+        _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), _ptr(q_out), _ptr(k_out), _ptr(status),
+        s))
+
+
+def pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, cos, sin, pos, dq_out, dk_out, dq, dk,
+                          dq_weight, dk_weight, workspace, status, stream=None):
+    """Gradients of pbsa_qk_norm_rope; dq_weight, dk_weight may be None."""
+    dt = _TORCH.get(cfg.dtype)
+    if not cfg.Hkv:
+        k = dk_out = dk = None
+    dev = _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, _TORCH.get(cfg.grad_dtype)),
+                          ("d", dq, dk, dt)), q_weight, k_weight, cos, sin, pos, status)
+    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if w is not None:
+            _want(w, name, (cfg.D,), torch.float32, dev)
+    _want_workspace(workspace, dev)
+    _launch(dev, stream, lambda s: _lib.pbsa_qk_norm_rope_bwd(
+        _cfg(cfg), _ptr(q), _ptr(k), _strides(q, k, dq_out, dk_out, dq, dk), _ptr(q_weight),
+        _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
+        _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace), _bytes(workspace),
+        _ptr(status), s))
+
+
+def pbsa_validate_kv4_config(cfg):
+    _check(_lib.pbsa_validate_kv4_config(_cfg(cfg)))
+
+
+def pbsa_kv4_workspace_size(cfg, T: int) -> int:
+    n = _lib.pbsa_kv4_workspace_size(_cfg(cfg), T)
+    if n == 0 and T != 0:
+        raise PBSAError(PBSA_ERR_ARG, pbsa_last_error())
+    return n
+
+
+def _kv4_check(cfg, cache, status):
+    if cache.shape != (cfg.B, cfg.Hkv, cfg.capacity, cfg.D):
+        _bad(f"cache of shape {cache.shape} does not belong to this configuration")
+    if status is not None:
+        _want(status, "status", (1,), torch.int32, cache.device)
+    return cache.device
+
+
+def pbsa_kv4_append(cfg, cache, k_new, v_new, pos_new, rows, mass, status, stream=None):
+    """Quantises the new tokens' keys and values into `rows` (None: row = position)."""
+    dev = _kv4_check(cfg, cache, status)
+    T = k_new.shape[1]
+    _want(k_new, "k_new", (cfg.B, T, cfg.Hkv, cfg.D), _TORCH.get(cfg.dtype), dev, True)
+    _want(v_new, "v_new", k_new.shape, k_new.dtype, dev, True)
+    _want(pos_new, "pos_new", (cfg.B, T), torch.int32, dev)
+    if rows is not None:
+        _want(rows, "rows", (cfg.B, cfg.Hkv, T), torch.int32, dev)
+    if mass is not None:
+        _want(mass, "mass", (cfg.B, cfg.Hkv, cfg.capacity), torch.float32, dev)
+    _launch(dev, stream, lambda s: _lib.pbsa_kv4_append(
+        _cfg(cfg), ctypes.byref(cache), _ptr(k_new), _ptr(v_new), _strides(k_new, v_new), T,
+        _ptr(pos_new), _ptr(rows), _ptr(mass), _ptr(status), s))
+
+
+def pbsa_kv4_read(cfg, cache, rows, k_out, v_out, status, stream=None):
+    """The values of the given rows (None: the first k_out.shape[2] rows)."""
+    dev = _kv4_check(cfg, cache, status)
+    n = k_out.shape[2]
+    _want(k_out, "k_out", (cfg.B, cfg.Hkv, n, cfg.D), _TORCH.get(cfg.dtype), dev)
+    _want(v_out, "v_out", k_out.shape, k_out.dtype, dev)
+    if rows is not None:
+        _want(rows, "rows", (cfg.B, cfg.Hkv, n), torch.int32, dev)
+    _launch(dev, stream, lambda s: _lib.pbsa_kv4_read(
+        _cfg(cfg), ctypes.byref(cache), _ptr(rows), n, _ptr(k_out), _ptr(v_out),
+        _ptr(status), s))
+
+
+def pbsa_kv4_attn(cfg, cache, q, q_pos, kv_len, out, lse, mass, workspace, status, stream=None):
+    """Attention of q [B, T, Hq, D] over the cache; q_pos and mass may be None."""
+    dev = _kv4_check(cfg, cache, status)
+    T = q.shape[1]
+    _want(q, "q", (cfg.B, T, cfg.Hq, cfg.D), _TORCH.get(cfg.dtype), dev, True)
+    _want(out, "out", q.shape, q.dtype, dev)
+    _want(lse, "lse", (cfg.B, cfg.Hq, T), torch.float32, dev)
+    _want(kv_len, "kv_len", (cfg.B,), torch.int32, dev)
+    if q_pos is not None:
+        _want(q_pos, "q_pos", (cfg.B, T), torch.int32, dev)
+    if mass is not None:
+        _want(mass, "mass", (cfg.B, cfg.Hkv, cfg.capacity), torch.float32, dev)
+    _want_workspace(workspace, dev)
+    _launch(dev, stream, lambda s: _lib.pbsa_kv4_attn(
+        _cfg(cfg), ctypes.byref(cache), _ptr(q), _strides(q), T, _ptr(q_pos), _ptr(kv_len),
+        _ptr(out), _ptr(lse), _ptr(mass), _ptr(workspace), _bytes(workspace), _ptr(status), s))
+
+
+def pbsa_kv4_evict(cfg, pos, mass, n_sink, keep_from, rows, status, stream=None):
+    """Chooses rows.shape[2] rows of every sequence and key head for the next tokens."""
+    dev = pos.device
+    shape = (cfg.B, cfg.Hkv, cfg.capacity)
+    _want(pos, "pos", shape, torch.int32, dev)
+    _want(mass, "mass", shape, torch.float32, dev)
+    n = rows.shape[2]
+    _want(rows, "rows", (cfg.B, cfg.Hkv, n), torch.int32, dev)
+    if keep_from is not None:
+        _want(keep_from, "keep_from", (cfg.B,), torch.int32, dev)
+    _want(status, "status", (1,), torch.int32, dev)
+    _launch(dev, stream, lambda s: _lib.pbsa_kv4_evict(
+        _cfg(cfg), _ptr(pos), _ptr(mass), n, n_sink, _ptr(keep_from), _ptr(rows), _ptr(status), s))

@@ -1,0 +1,88 @@
+"""A bounded 4-bit cache of single tokens: attend, account, evict (include/pbsa.h, token cache).
+
+Beside ``SparseForcingAttention``, whose caches hold blocks of video tokens in bf16, this one
+holds tokens one by one, for streams that are generated token by token or in small steps.  The
+object owns the device tensors; every step of the method runs in the kernels behind
+``pbsa.pbsa_kv4_*``.
+
+    cache = TokenCache(B, Hq, Hkv, D, capacity=4096, n_sink=4, n_recent=256)
+    out = cache.step(q, k, v)        # rows for the new tokens, append, causal attention
+
+Until the cache is full the new tokens take empty rows; then they take the rows that drew the
+least attention so far, sparing the sequence's first ``n_sink`` and its last ``n_recent`` tokens.
+(A padded sequence of the step that fills the cache may give up a row while an empty one is left:
+the chosen rows are taken in row order.)
+Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph (run one
+before, so that its buffers exist)."""
+from __future__ import annotations
+
+import torch
+
+from . import pbsa as P
+
+
+class TokenCache:
+    def __init__(self, B: int, Hq: int, Hkv: int, D: int, capacity: int, dtype=torch.bfloat16,
+                 n_sink: int = 4, n_recent: int = 64, k_unit: float = 1.0, v_unit: float = 1.0,
+                 device="cuda"):
+        self.cfg = P.make_kv4_config(B, Hq, Hkv, D, capacity, dtype, k_unit, v_unit)
+        P.pbsa_validate_kv4_config(self.cfg)
+        if n_sink < 0 or n_recent < 0:
+            raise ValueError("n_sink and n_recent must be >= 0")
+        self.B, self.Hq, self.Hkv, self.D, self.capacity = B, Hq, Hkv, D, capacity
+        self.dtype, self.n_sink, self.n_recent = dtype, n_sink, n_recent
+        dev = self.device = torch.device(device)
+        u8 = dict(dtype=torch.uint8, device=dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        rows = (B, Hkv, capacity)
+        self.k_codes = torch.zeros(*rows, D // 2, **u8)
+        self.k_scales = torch.zeros(*rows, D // 16, **u8)
+        self.v_codes = torch.zeros(*rows, D // 2, **u8)
+        self.v_scales = torch.zeros(*rows, D // 16, **u8)
+        self.pos = torch.full(rows, -1, **i32)
+        self.mass = torch.zeros(*rows, dtype=torch.float32, device=dev)
+        self.cache = P.make_kv4_cache(self.cfg, self.k_codes, self.k_scales, self.v_codes,
+                                      self.v_scales, self.pos)
+        self.device = self.pos.device
+        self.seen = torch.zeros(B, **i32)       # tokens of every sequence so far
+        self.kv_len = torch.zeros(B, **i32)     # rows in use
+        self.status = torch.zeros(1, **i32)
+        self._steps = {}
+
+    def _buffers(self, T: int):
+        """The tensors of a step of T tokens, allocated on its first use."""
+        if T not in self._steps:
+            dev = self.device
+            self._steps[T] = dict(
+                ar=torch.arange(T, dtype=torch.int32, device=dev),
+                rows=torch.empty(self.B, self.Hkv, T, dtype=torch.int32, device=dev),
+                out=torch.empty(self.B, T, self.Hq, self.D, dtype=self.dtype, device=dev),
+                lse=torch.empty(self.B, self.Hq, T, dtype=torch.float32, device=dev),
+                ws=torch.empty(P.pbsa_kv4_workspace_size(self.cfg, T), dtype=torch.uint8,
+                               device=dev))
+        return self._steps[T]
+
+    def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_new=None):
+        """T new tokens of every sequence (n_new [B] int32 on the device: how many of them are
+        tokens, the rest is padding; None: all) enter the cache and attend to it and to each
+        other causally.  q [B, T, Hq, D], k, v [B, T, Hkv, D], normalised and rotated already.
+        Returns the output buffer [B, T, Hq, D] (zeros for padding)."""
+        T = q.shape[1]
+        if T + self.n_sink + self.n_recent > self.capacity:
+            raise ValueError(f"a step of {T} tokens does not fit beside {self.n_sink} sink and "
+                             f"{self.n_recent} recent tokens in {self.capacity} rows")
+        s = self._buffers(T)
+        pos = self.seen[:, None] + s["ar"]
+        n = T
+        if n_new is not None:
+            n = n_new
+            pos = torch.where(s["ar"] < n_new[:, None], pos, torch.full_like(pos, -1))
+        P.pbsa_kv4_evict(self.cfg, self.pos, self.mass, self.n_sink, self.seen - self.n_recent,
+                         s["rows"], self.status)
+        P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, s["rows"], self.mass, self.status)
+        self.seen += n
+        self.kv_len += n
+        self.kv_len.clamp_(max=self.capacity)
+        P.pbsa_kv4_attn(self.cfg, self.cache, q, pos, self.kv_len, s["out"], s["lse"], self.mass,
+                        s["ws"], self.status)
+        return s["out"]

@@ -325,6 +325,181 @@ PBSA_API int pbsa_cache_update(const pbsa_config* cfg, const void* k_local, cons
                       int32_t* pers_src, int32_t* upd, int32_t* n_upd,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------- heads: norm and rotation */
+
+/* Types of tensors whose type is a choice (pbsa_qk_config, pbsa_kv4_config). */
+#define PBSA_DTYPE_BF16 0
+#define PBSA_DTYPE_FP16 1
+#define PBSA_DTYPE_FP32 2
+
+/*
+ * The step before the cache: every query and key head is RMS-normalised over its D channels,
+ * scaled by a weight of D entries (one for queries, one for keys, shared by their heads) and
+ * rotated by its token's position.  The project page starts from ready queries and keys;
+ * this step is this library's.
+ *
+ *   r = (mean_i x_i^2 + eps)^(-1/2),  n_i = x_i r w_i,  and for every rotated pair (a, b) of
+ *   n and its angle:  a' = a cos - b sin,  b' = b cos + a sin.
+ *
+ * The first rot_dim channels are rotated (0: none), in pairs (2i, 2i+1) when `interleaved`,
+ * else (i, i + rot_dim/2).  A token's position has n_axes components (1 for text; frame, row
+ * and column for video): the first axis_pairs[0] pairs turn by component 0, the next
+ * axis_pairs[1] by component 1, and so on.  Pair i of a token at component p turns by the
+ * angle whose cosine and sine are cos[p][i] and sin[p][i].
+ */
+typedef struct pbsa_qk_config {
+    int B, T;            /* sequences, tokens of each (0 is allowed) */
+    int Hq, Hkv;         /* query heads >= 1, key heads >= 0 (0: queries only, key pointers NULL) */
+    int D;               /* head dim, 64 or 128 */
+    int dtype;           /* PBSA_DTYPE_* of q, k, q_out, k_out, dq, dk */
+    int grad_dtype;      /* of dq_out and dk_out: dtype or PBSA_DTYPE_FP32 */
+    int rot_dim;         /* a multiple of 16 in [0, D] */
+    int interleaved;     /* pairing, see above */
+    int n_axes;          /* 1..3 */
+    int axis_pairs[3];   /* sum over the n_axes used = rot_dim / 2 */
+    int table_len;       /* rows of cos and sin */
+    float eps;           /* > 0 */
+} pbsa_qk_config;
+
+/* Workspace bytes of pbsa_qk_norm_rope_bwd (0 on a bad configuration). */
+PBSA_API size_t pbsa_qk_workspace_size(const pbsa_qk_config* cfg);
+
+/*
+ *   q, q_out [B, T, Hq, D], k, k_out [B, T, Hkv, D] of cfg->dtype
+ *   strides  NULL (all contiguous) or 12 strides in elements: batch, token and head of q, k,
+ *            q_out, k_out in that order (channels are contiguous; every stride a multiple of
+ *            16 bytes).  Views of one projection's output are read in place.  An output may
+ *            be its own input (same pointer and strides), else they must not overlap.
+ *   wq, wk   nullable (all ones); [D] fp32
+ *   cos, sin [table_len, rot_dim / 2] fp32, pos [B, T, n_axes] int32; NULL when rot_dim is 0
+ *   status   device int32; a position outside [0, table_len) records PBSA_ERR_DEVICE_CHECK
+ *            and that token's outputs are left as they were.  May be NULL when rot_dim is 0.
+ */
+PBSA_API int pbsa_qk_norm_rope(const pbsa_qk_config* cfg, const void* q, const void* k,
+                               const int64_t* strides, const float* wq, const float* wk,
+                               const float* cos, const float* sin, const int32_t* pos,
+                               void* q_out, void* k_out, int32_t* status, void* stream);
+
+/*
+ * Gradients of sum(q_out * dq_out) + sum(k_out * dk_out).
+ *
+ *   dq_out, dk_out  gradients of the outputs, of cfg->grad_dtype (pbsa_attn_bwd gives fp32)
+ *   dq, dk          gradients of q and k out, of cfg->dtype
+ *   dwq, dwk        nullable; [D] fp32 out (overwritten), summed over tokens and heads in a
+ *                   fixed order: two runs on one kind of GPU agree bit for bit
+ *   strides         NULL or 18: of q, k, dq_out, dk_out, dq, dk; dq may be dq_out (same
+ *                   pointer, strides and type), likewise dk
+ *   workspace >= pbsa_qk_workspace_size(cfg) bytes when dwq or dwk is given
+ * A token whose position is out of range is left out: its dq, dk stay as they were.
+ */
+PBSA_API int pbsa_qk_norm_rope_bwd(const pbsa_qk_config* cfg, const void* q, const void* k,
+                                   const int64_t* strides, const float* wq, const float* wk,
+                                   const float* cos, const float* sin, const int32_t* pos,
+                                   const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                   float* dwq, float* dwk, void* workspace,
+                                   size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ------------------------------------------------------------ token cache in 4 bits */
+
+/*
+ * A cache of single tokens beside the block caches: `capacity` rows per (sequence, key head),
+ * each one token's key and value in 4 bits.  Rows are in no order; pos says which token a row
+ * holds.  Keys are stored as they are attended (normalised and rotated).
+ *
+ * Sixteen consecutive channels share a scale: value = unit * e4m3(scale) * e2m1(code), unit a
+ * power of two for the whole cache.  scale is amax / 6 / unit rounded to e4m3 (at most 448),
+ * a code the nearest of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} to x / unit / e4m3(scale), ties to the
+ * even code.  Every value is exact in bf16 and in fp16 (unit 1), so that attending reads what
+ * was stored without another rounding.  Infinities saturate; a NaN is stored as zero and
+ * records PBSA_ERR_DEVICE_CHECK: a cache row is always finite.
+ */
+typedef struct pbsa_kv4_config {
+    int B, Hq, Hkv, D;     /* Hq a multiple of Hkv: query head h reads key head h / (Hq / Hkv) */
+    int capacity;          /* N, rows; a multiple of 64 */
+    int dtype;             /* PBSA_DTYPE_BF16 or _FP16: queries, new keys and values, outputs */
+    float k_unit, v_unit;  /* powers of two in [2^-40, 2^40] */
+} pbsa_kv4_config;
+
+/* The cache's device tensors (the caller's). */
+typedef struct pbsa_kv4_cache {
+    uint8_t* k_codes;   /* [B, Hkv, N, D / 2]; channel 2i in the low nibble of byte i */
+    uint8_t* k_scales;  /* [B, Hkv, N, D / 16], e4m3, finite */
+    uint8_t* v_codes;   /* as the keys' */
+    uint8_t* v_scales;
+    int32_t* pos;       /* [B, Hkv, N]: position of the row's token, -1 = empty row */
+} pbsa_kv4_cache;
+
+PBSA_API int pbsa_validate_kv4_config(const pbsa_kv4_config* cfg);
+/* Workspace bytes of pbsa_kv4_attn for T query tokens (0 on a bad configuration). */
+PBSA_API size_t pbsa_kv4_workspace_size(const pbsa_kv4_config* cfg, int T);
+
+/*
+ * Quantises T new tokens of every sequence into given rows.
+ *
+ *   k_new, v_new [B, T, Hkv, D]; strides NULL or 6 (batch, token, head of k_new, then v_new)
+ *   pos_new [B, T] int32: the tokens' positions; a negative one is no token (the padding of a
+ *            shorter sequence): nothing is written for it
+ *   rows     nullable; [B, Hkv, T] int32, the rows to write (pbsa_kv4_evict gives them);
+ *            those of one sequence and head must differ.  NULL: token at position p to row p,
+ *            a cache that keeps every token.
+ *   mass     nullable; [B, Hkv, N] fp32: the written rows' entries become 0
+ *   status   a row outside [0, N) records PBSA_ERR_DEVICE_CHECK and is skipped
+ */
+PBSA_API int pbsa_kv4_append(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cache,
+                             const void* k_new, const void* v_new, const int64_t* strides, int T,
+                             const int32_t* pos_new, const int32_t* rows, float* mass,
+                             int32_t* status, void* stream);
+
+/*
+ * The values that rows stand for, e.g. for a kernel that reads bf16 keys.
+ *
+ *   rows  nullable; [B, Hkv, n] int32.  NULL: rows 0 .. n-1 (n <= N)
+ *   k_out, v_out [B, Hkv, n, D] of cfg->dtype.  Row -1 (none) gives zeros; any other row
+ *   outside [0, N) does too, and records PBSA_ERR_DEVICE_CHECK.
+ */
+PBSA_API int pbsa_kv4_read(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cache,
+                           const int32_t* rows, int n, void* k_out, void* v_out, int32_t* status,
+                           void* stream);
+
+/*
+ * Attention of T query tokens of every sequence over its cache, softmax scale 1/sqrt(D).
+ *
+ * Row j of (b, key head) is seen by query t when j < kv_len[b], pos[j] >= 0 and, with q_pos,
+ * pos[j] <= q_pos[b][t].  A query that sees no row (an empty cache; q_pos -1, the padding of a
+ * shorter sequence) gets out = 0 and lse = -infinity.
+ *
+ *   q        [B, T, Hq, D]; strides NULL or 3 (batch, token, head)
+ *   q_pos    nullable; [B, T] int32, the causal mask above
+ *   kv_len   [B] int32: rows in use; outside [0, N] it is clamped and PBSA_ERR_DEVICE_CHECK
+ *            recorded
+ *   out      [B, T, Hq, D] contiguous, lse [B, Hq, T] fp32 (natural logarithm)
+ *   mass     nullable; [B, Hkv, N] fp32, accumulated (+=): every row's softmax probability
+ *            summed over the call's queries and the key head's query heads, in a fixed order
+ *   workspace >= pbsa_kv4_workspace_size(cfg, T) bytes; calls that may overlap on the GPU need
+ *            their own
+ */
+PBSA_API int pbsa_kv4_attn(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cache, const void* q,
+                           const int64_t* strides, int T, const int32_t* q_pos,
+                           const int32_t* kv_len, void* out, float* lse, float* mass,
+                           void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Chooses the rows that the next n tokens of every (sequence, key head) take: empty rows
+ * (pos < 0) first, in row order, then the rows with the least accumulated mass, ties to the
+ * lower row.  A row whose token is among the first n_sink of the sequence (pos < n_sink) or
+ * not older than keep_from[b] (pos >= keep_from[b]) is never chosen.  Negative masses count
+ * as 0, NaN as the greatest.  Nothing but `rows` is written: the rows stay readable until
+ * pbsa_kv4_append overwrites them.
+ *
+ *   pos, mass  [B, Hkv, N]
+ *   keep_from  nullable (no row is too young); [B] int32
+ *   rows       [B, Hkv, n] int32 out, ascending; where fewer than n rows may go, the rest is
+ *              -1 and PBSA_ERR_DEVICE_CHECK is recorded
+ */
+PBSA_API int pbsa_kv4_evict(const pbsa_kv4_config* cfg, const int32_t* pos, const float* mass, int n,
+                            int n_sink, const int32_t* keep_from, int32_t* rows, int32_t* status,
+                            void* stream);
+
 /*
  * Diagnostic: runs one kernel that waits, with the library's bounded wait, on a barrier
  * that nothing completes.  After `timeout_ns` nanoseconds the wait gives up and writes
