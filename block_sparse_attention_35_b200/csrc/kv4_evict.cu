@@ -3,11 +3,18 @@
 // Every row gets a 32-bit key: 0 when it is empty, all ones when it is protected (a first
 // token of the sequence or a recent one), else one more than the bits of its accumulated mass
 // (non-negative floats order as their bits do).  The n rows with the smallest (key, row) are
-// wanted, in row order: the n-th smallest key is found by a radix select, 8 bits a round, then
-// one ordered sweep writes the rows below it and the first of those that equal it.
+// wanted, in row order.
 //
-// Bound: the masses and positions are read once from HBM (8 bytes a row); later rounds find
-// them in L2.
+// Bound: the masses and positions are read once from HBM, 8 bytes a row.  A cluster of one to
+// eight CTAs holds all keys of a (sequence, key head) in registers; a warp owns consecutive
+// rows.  The n-th smallest key is found by a radix select in three rounds (11, 11 and 10 bits)
+// with histograms in shared memory: only the keys that share the digits found so far take part
+// in a round, so nearly all of the work is the first, and 11 bits of a float tell octaves and
+// quarters apart, which keeps the histogram's adds off each other.  Two sweeps over the
+// registers then count and write the rows in order: the counts of a warp need no barrier, and
+// one exchange between the warps and CTAs places them.
+#include <cooperative_groups.h>
+
 #include "pbsa_device.cuh"
 #include "token_internal.cuh"
 
@@ -15,7 +22,12 @@ namespace pbsa {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
 constexpr uint32_t kProtected = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t row_key(int pos, float mass, int n_sink, int keep_from) {
@@ -25,97 +37,215 @@ __device__ __forceinline__ uint32_t row_key(int pos, float mass, int n_sink, int
     return __float_as_uint(fmaxf(mass, 0.f) + 0.f) + 1u;   // + 0: no negative zero
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a) {
-    __shared__ unsigned hist[256];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_rank, s_warp_lt[32], s_warp_eq[32];
-    const int bh = blockIdx.x, b = bh / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Inclusive sum over the block of one value a thread; `sums` is shared scratch of kWarps.
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    unsigned before = lane < warp ? sums[lane] : 0u;
+    before = __reduce_add_sync(0xffffffffu, before);
+    return v + before;
+}
+
+// K > 0: a thread keeps K keys; K = 0: `tiles` of them, read again in every round (a cache of
+// more than kMaxCluster x 24576 rows).
+template <int K>
+__global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a, int tiles) {
+    __shared__ unsigned hist[kBins];
+    __shared__ unsigned sums[kWarps];
+    __shared__ unsigned s_lt[kWarps], s_eq[kWarps];
+    __shared__ unsigned s_cta[kMaxCluster][2];   // every CTA's counts below and equal to the threshold
+    __shared__ unsigned s_found[2];              // prefix and rank, from the first CTA
+    __shared__ unsigned long long s_min[kMaxCluster][kWarps];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int bh = blockIdx.x / ctas, b = bh / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t* pos = a.pos + (size_t)bh * a.N;
     const float* mass = a.mass + (size_t)bh * a.N;
     const int keep_from = a.keep_from ? a.keep_from[b] : 0x7fffffff;
     int32_t* rows = a.rows + (size_t)bh * a.n;
+    const int per = K > 0 ? K : tiles;
+    const int row0 = (rank * kWarps + warp) * per * 32 + lane;   // this thread's rows: row0 + 32 j
+
+    uint32_t keys[K > 0 ? K : 1];
+    if (K > 0) {
+        constexpr int kGroup = K > 8 ? 6 : K;   // loads in flight: twice as many
+#pragma unroll
+        for (int j0 = 0; j0 < K; j0 += kGroup) {
+            int p[kGroup > 0 ? kGroup : 1];
+            float m[kGroup > 0 ? kGroup : 1];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const int i = row0 + 32 * (j0 + j);
+                p[j] = i < a.N ? pos[i] : -1;
+                m[j] = i < a.N ? mass[i] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                keys[j0 + j] = row0 + 32 * (j0 + j) < a.N ? row_key(p[j], m[j], a.n_sink, keep_from) : kProtected;
+        }
+    }
+    auto key = [&](int j) -> uint32_t {
+        if (K > 0) return keys[K > 0 ? j : 0];
+        const int i = row0 + 32 * j;
+        return i < a.N ? row_key(pos[i], mass[i], a.n_sink, keep_from) : kProtected;
+    };
+
+    if (a.n == 1) {   // the smallest (key, row) alone: no select
+        unsigned long long best = ~0ull;
+#pragma unroll
+        for (int j = 0; j < per; ++j) best = min(best, ((unsigned long long)key(j) << 32) | (unsigned)(row0 + 32 * j));
+        const unsigned hi = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32));
+        const unsigned lo = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32) == hi ? (unsigned)best : 0xffffffffu);
+        if (ctas > 1) cluster.sync();   // the first CTA runs before its memory is written
+        if (lane == 0) cluster.map_shared_rank(&s_min[rank][warp], 0)[0] = ((unsigned long long)hi << 32) | lo;
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+        if (rank == 0 && warp == 0) {
+            best = ~0ull;
+            for (int r = 0; r < ctas; ++r) best = min(best, s_min[r][lane]);
+            const unsigned h = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32));
+            const unsigned l = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32) == h ? (unsigned)best : 0xffffffffu);
+            if (lane == 0) {
+                rows[0] = h == kProtected ? -1 : (int)l;
+                if (h == kProtected) set_status(a.status, PBSA_ERR_DEVICE_CHECK);
+            }
+        }
+        return;
+    }
 
     // radix select: the n-th smallest key, and its rank among the keys equal to it
-    uint32_t prefix = 0;
-    int rank = a.n;   // 1-based rank within the keys that match the prefix so far
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < a.N; i += kThreads) {
-            const uint32_t k = row_key(pos[i], mass[i], a.n_sink, keep_from);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    uint32_t prefix = 0, known = 0;   // digits found so far, and their mask
+    unsigned want = a.n;              // 1-based rank among the keys with these digits
+    for (int round = 0; round < 3; ++round) {
+        const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0), bits = round == 2 ? 10 : 11;
+        const uint32_t mask = (1u << bits) - 1u;
+        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+#pragma unroll
+        for (int j = 0; j < per; ++j) {
+            const uint32_t k = key(j);
+            const bool in = (k & known) == prefix && row0 + 32 * j < a.N;
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (who == 0) continue;
+            const unsigned digit = (k >> shift) & mask;
+            // a warp of one digit (new rows' zero masses, protected rows) adds once
+            const unsigned lead = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+            if (__ballot_sync(0xffffffffu, in && digit != lead) == 0) {
+                if (lane == 0) atomicAdd(&hist[lead], (unsigned)__popc(who));
+            } else if (in) {
+                atomicAdd(&hist[digit], 1u);
+            }
         }
         __syncthreads();
-        if (warp == 0) {
-            unsigned c[8], sum = 0;
-            for (int j = 0; j < 8; ++j) sum += (c[j] = hist[lane * 8 + j]);
-            unsigned incl = sum;
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
+        if (ctas > 1) {
+            if (rank > 0) {
+                unsigned* h0 = cluster.map_shared_rank(hist, 0);
+                for (int i = tid; i < kBins; i += kThreads)
+                    if (hist[i]) atomicAdd(&h0[i], hist[i]);
             }
-            unsigned before = incl - sum;
-            if (before < (unsigned)rank && (unsigned)rank <= incl) {
-                for (int j = 0; j < 8; ++j) {
-                    if ((unsigned)rank <= before + c[j]) {
-                        s_prefix = prefix | ((uint32_t)(lane * 8 + j) << shift);
-                        s_rank = rank - (int)before;
-                        break;
-                    }
-                    before += c[j];
+            cluster.sync();
+        }
+        if (rank == 0) {
+            const unsigned c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
+            const unsigned upto = block_scan(c0 + c1, sums), before = upto - c0 - c1;
+            if (before < want && want <= upto) {
+                const bool second = want > before + c0;
+                const unsigned found[2] = {prefix | ((unsigned)(2 * tid + second) << shift),
+                                           want - before - (second ? c0 : 0u)};
+                for (int r = 0; r < ctas; ++r) {
+                    unsigned* f = cluster.map_shared_rank(s_found, r);
+                    f[0] = found[0];
+                    f[1] = found[1];
                 }
             }
         }
-        __syncthreads();
-        prefix = s_prefix;
-        rank = s_rank;
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+        prefix = s_found[0];
+        want = s_found[1];
+        known |= mask << shift;
     }
     const uint32_t tau = prefix;
-    const int quota = tau == kProtected ? 0 : rank;   // rows equal to tau that are taken
+    const unsigned quota = tau == kProtected ? 0u : want;   // rows equal to tau that are taken
 
-    // ordered sweep
-    int out = 0, eq_seen = 0;
-    for (int i0 = 0; i0 < a.N; i0 += kThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < a.N ? row_key(pos[i], mass[i], a.n_sink, keep_from) : kProtected;
-        const bool lt = k < tau, eq = k == tau && i < a.N;
-        const unsigned mlt = __ballot_sync(0xffffffffu, lt), meq = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            s_warp_lt[warp] = __popc(mlt);
-            s_warp_eq[warp] = __popc(meq);
-        }
-        __syncthreads();
-        int lt_before = 0, eq_before = eq_seen, lt_all = 0, eq_all = 0;
-        for (int w = 0; w < 32; ++w) {
-            const int l = s_warp_lt[w], e = s_warp_eq[w];
-            if (w < warp) {
-                lt_before += l;
-                eq_before += e;
-            }
-            lt_all += l;
-            eq_all += e;
-        }
-        const unsigned below = (1u << lane) - 1u;
-        lt_before += __popc(mlt & below);
-        eq_before += __popc(meq & below);
-        // rows written before this one: smaller keys, and equal ones within the quota
-        const int at = out + lt_before + (min(eq_before, quota) - min(eq_seen, quota));
-        if (lt || (eq && eq_before < quota)) rows[at] = i;
-        out += lt_all + min(eq_seen + eq_all, quota) - min(eq_seen, quota);
-        eq_seen += eq_all;
-        __syncthreads();
+    // counts of every warp, then the rows below tau and the first of those equal to it
+    unsigned lt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < per; ++j) {
+        const uint32_t k = key(j);
+        lt += __popc(__ballot_sync(0xffffffffu, k < tau));
+        eq += __popc(__ballot_sync(0xffffffffu, k == tau));
     }
-    if (out < a.n) {
-        for (int i = out + tid; i < a.n; i += kThreads) rows[i] = -1;
+    if (lane == 0) {
+        s_lt[warp] = lt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned l = __reduce_add_sync(0xffffffffu, s_lt[lane]), e = __reduce_add_sync(0xffffffffu, s_eq[lane]);
+        if (lane < ctas) {
+            unsigned* d = cluster.map_shared_rank(&s_cta[rank][0], lane);
+            d[0] = l;
+            d[1] = e;
+        }
+    }
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+    unsigned lt_at = __reduce_add_sync(0xffffffffu, (lane < warp ? s_lt[lane] : 0u) + (lane < rank ? s_cta[lane][0] : 0u));
+    unsigned eq_at = __reduce_add_sync(0xffffffffu, (lane < warp ? s_eq[lane] : 0u) + (lane < rank ? s_cta[lane][1] : 0u));
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+    for (int j = 0; j < per; ++j) {
+        const uint32_t k = key(j);
+        const unsigned ml = __ballot_sync(0xffffffffu, k < tau), me = __ballot_sync(0xffffffffu, k == tau);
+        const unsigned l = lt_at + __popc(ml & below), e = eq_at + __popc(me & below);
+        if (k < tau || (k == tau && e < quota)) rows[l + min(e, quota)] = row0 + 32 * j;
+        lt_at += __popc(ml);
+        eq_at += __popc(me);
+    }
+    if (tau == kProtected && rank == 0) {   // fewer than n rows may go
+        unsigned all = __reduce_add_sync(0xffffffffu, lane < ctas ? s_cta[lane][0] : 0u);
+        for (int i = all + tid; i < a.n; i += kThreads) rows[i] = -1;
         if (tid == 0) set_status(a.status, PBSA_ERR_DEVICE_CHECK);
     }
+}
+
+template <int K>
+cudaError_t run(const EvictArgs& a, int ctas, int tiles, cudaStream_t st) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.BH * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_kernel<K>, a, tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
-    evict_kernel<<<a.BH, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    const int tiles = (a.N + kThreads - 1) / kThreads;   // keys of a thread, with one CTA
+    if (tiles <= 2) return run<2>(a, 1, 0, st);
+    auto cluster = [&](int keys) {
+        int ctas = 1;
+        while (keys * ctas < tiles) ctas *= 2;
+        return ctas;
+    };
+    // few heads: more CTAs for each
+    if (tiles <= 8 * kMaxCluster && (tiles <= 8 || a.BH * cluster(8) <= kSMs)) return run<8>(a, cluster(8), 0, st);
+    if (tiles <= 24 * kMaxCluster) return run<24>(a, cluster(24), 0, st);
+    return run<0>(a, kMaxCluster, (tiles + kMaxCluster - 1) / kMaxCluster, st);
 }
 
 }  // namespace pbsa

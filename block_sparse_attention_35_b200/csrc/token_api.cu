@@ -86,6 +86,7 @@ int validate(const pbsa_kv4_config* c) {
     if (c->D != 64 && c->D != 128) return api_failf(PBSA_ERR_UNSUPPORTED, "head dim %d: only 64 and 128 are built", c->D);
     if (c->capacity < 64 || c->capacity % 64)
         return api_failf(PBSA_ERR_ARG, "capacity %d is not a positive multiple of 64", c->capacity);
+    if (c->capacity > (1 << 24)) return api_failf(PBSA_ERR_UNSUPPORTED, "capacity %d above 2^24", c->capacity);
     if ((long long)c->B * c->Hkv * (c->capacity / 64) > 0x7fffffffll)
         return api_failf(PBSA_ERR_UNSUPPORTED, "cache of more than 2^31 64-row groups");
     if (c->dtype != PBSA_DTYPE_BF16 && c->dtype != PBSA_DTYPE_FP16)
@@ -112,7 +113,7 @@ int check_cache(const pbsa_kv4_cache* cache) {
 // Tokens of a kv4 call: the grid and index types hold for these.
 int check_tokens(const pbsa_kv4_config* c, int T) {
     if (T < 0) return api_failf(PBSA_ERR_ARG, "T %d < 0", T);
-    if ((long long)T * (c->Hq / c->Hkv) > (1 << 20) || (long long)c->B * T * c->Hq * (c->D / 16) > (1ll << 36))
+    if ((long long)T * (c->Hq / c->Hkv) > (1 << 20) || (long long)c->B * T * c->Hq > 0x7fffffffll)
         return api_failf(PBSA_ERR_UNSUPPORTED, "T %d: too many query rows in one call", T);
     return PBSA_OK;
 }

@@ -116,7 +116,7 @@ def make_kv4_cache(cfg, k_codes, k_scales, v_codes, v_scales, pos) -> pbsa_kv4_c
     c = pbsa_kv4_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                        v_scales.data_ptr(), pos.data_ptr())
     c.tensors = (k_codes, k_scales, v_codes, v_scales, pos)
-    c.device = dev
+    c.device, c.index = dev, pos.get_device()
     c.shape = (cfg.B, cfg.Hkv, cfg.capacity, cfg.D)
     return c
 
@@ -385,15 +385,29 @@ def _strides(*tensors):
     return out
 
 
-def _launch(device, stream, call):
-    """Runs call(stream) with the tensors' device current; its own stream unless one is given."""
-    if device.type != "cuda":
-        _bad(f"tensors are on {device}, not on a CUDA device")
-    if torch.cuda.current_device() == device.index:
-        _check(call(_stream(stream)))
+# what torch.cuda.current_stream() and current_device() ask, without the objects around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _launch(index, stream, call, *args):
+    """call(*args, stream) with device `index` current; its current stream unless one is given."""
+    if index < 0:
+        _bad("tensors are not on a CUDA device")
+    if _current_device() == index:
+        rc = call(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
-            _check(call(_stream(stream)))
+        with torch.cuda.device(index):
+            rc = call(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if rc != PBSA_OK:
+        _check(rc)
+
+
+def _ok(t, shape, dtype, index):
+    """Whether a tensor is as it nearly always is; the caller looks closer where it is not.
+    (These checks are most of what a call of a single token costs the host.)"""
+    return (t.shape == shape and t.dtype is dtype and t.get_device() == index and
+            t.is_contiguous())
 
 
 def _bytes(t):
@@ -436,37 +450,55 @@ def pbsa_qk_workspace_size(cfg) -> int:
     return n
 
 
+def _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status):
+    """The quick look at what both directions share."""
+    if (q_weight is None or k_weight is None or cos is None or sin is None or pos is None or
+            status is None or not cfg.Hkv):
+        return False
+    w, tab, f32 = (cfg.D,), (cfg.table_len, cfg.rot_dim // 2), torch.float32
+    return (_ok(q_weight, w, f32, i) and _ok(k_weight, w, f32, i) and _ok(cos, tab, f32, i) and
+            _ok(sin, tab, f32, i) and _ok(pos, (cfg.B, cfg.T, cfg.n_axes), torch.int32, i) and
+            _ok(status, (1,), torch.int32, i))
+
+
 def pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, pos, q_out, k_out, status,
                       stream=None):
     """RMS norm and rotation of every head; q, k, q_out, k_out may be strided views."""
-    dt = _TORCH.get(cfg.dtype)
-    if not cfg.Hkv:
-        k = k_out = None
-    dev = _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos,
-                    sin, pos, status)
-    _launch(dev, stream, lambda s: _lib.pbsa_qk_norm_rope(
-        _cfg(cfg), _ptr(q), _ptr(k), _strides(q, k, q_out, k_out), _ptr(q_weight),
-        _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), _ptr(q_out), _ptr(k_out), _ptr(status),
-        s))
+    dt, i, strides = _TORCH.get(cfg.dtype), q.get_device(), None
+    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
+    if not (_qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status) and _ok(q, sq, dt, i) and
+            _ok(k, sk, dt, i) and _ok(q_out, sq, dt, i) and _ok(k_out, sk, dt, i)):
+        if not cfg.Hkv:
+            k = k_out = None
+        _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos, sin,
+                  pos, status)
+        strides = _strides(q, k, q_out, k_out)
+    _launch(i, stream, _lib.pbsa_qk_norm_rope, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
+            _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), q_out.data_ptr(),
+            _ptr(k_out), _ptr(status))
 
 
 def pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, cos, sin, pos, dq_out, dk_out, dq, dk,
                           dq_weight, dk_weight, workspace, status, stream=None):
     """Gradients of pbsa_qk_norm_rope; dq_weight, dk_weight may be None."""
-    dt = _TORCH.get(cfg.dtype)
-    if not cfg.Hkv:
-        k = dk_out = dk = None
-    dev = _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, _TORCH.get(cfg.grad_dtype)),
-                          ("d", dq, dk, dt)), q_weight, k_weight, cos, sin, pos, status)
+    dt, gt, i, strides = _TORCH.get(cfg.dtype), _TORCH.get(cfg.grad_dtype), q.get_device(), None
+    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
+    if not (_qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status) and _ok(q, sq, dt, i) and
+            _ok(k, sk, dt, i) and _ok(dq_out, sq, gt, i) and _ok(dk_out, sk, gt, i) and
+            _ok(dq, sq, dt, i) and _ok(dk, sk, dt, i)):
+        if not cfg.Hkv:
+            k = dk_out = dk = None
+        _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)),
+                  q_weight, k_weight, cos, sin, pos, status)
+        strides = _strides(q, k, dq_out, dk_out, dq, dk)
     for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
         if w is not None:
-            _want(w, name, (cfg.D,), torch.float32, dev)
-    _want_workspace(workspace, dev)
-    _launch(dev, stream, lambda s: _lib.pbsa_qk_norm_rope_bwd(
-        _cfg(cfg), _ptr(q), _ptr(k), _strides(q, k, dq_out, dk_out, dq, dk), _ptr(q_weight),
-        _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
-        _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace), _bytes(workspace),
-        _ptr(status), s))
+            _want(w, name, (cfg.D,), torch.float32, q.device)
+    _want_workspace(workspace, q.device)
+    _launch(i, stream, _lib.pbsa_qk_norm_rope_bwd, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
+            _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), dq_out.data_ptr(),
+            _ptr(dk_out), dq.data_ptr(), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+            _bytes(workspace), _ptr(status))
 
 
 def pbsa_validate_kv4_config(cfg):
@@ -480,71 +512,84 @@ def pbsa_kv4_workspace_size(cfg, T: int) -> int:
     return n
 
 
-def _kv4_check(cfg, cache, status):
+def _kv4_check(cfg, cache):
     if cache.shape != (cfg.B, cfg.Hkv, cfg.capacity, cfg.D):
         _bad(f"cache of shape {cache.shape} does not belong to this configuration")
-    if status is not None:
-        _want(status, "status", (1,), torch.int32, cache.device)
-    return cache.device
+    return cache.device, cache.index
 
 
 def pbsa_kv4_append(cfg, cache, k_new, v_new, pos_new, rows, mass, status, stream=None):
     """Quantises the new tokens' keys and values into `rows` (None: row = position)."""
-    dev = _kv4_check(cfg, cache, status)
-    T = k_new.shape[1]
-    _want(k_new, "k_new", (cfg.B, T, cfg.Hkv, cfg.D), _TORCH.get(cfg.dtype), dev, True)
-    _want(v_new, "v_new", k_new.shape, k_new.dtype, dev, True)
-    _want(pos_new, "pos_new", (cfg.B, T), torch.int32, dev)
+    dev, i = _kv4_check(cfg, cache)
+    B, Hkv, T, dt, i32 = cfg.B, cfg.Hkv, k_new.shape[1], _TORCH.get(cfg.dtype), torch.int32
+    strides, shape = None, (B, T, Hkv, cfg.D)
+    if not (_ok(k_new, shape, dt, i) and _ok(v_new, shape, dt, i) and
+            _ok(pos_new, (B, T), i32, i) and _ok(status, (1,), i32, i)):
+        _want(k_new, "k_new", shape, dt, dev, True)
+        _want(v_new, "v_new", shape, dt, dev, True)
+        _want(pos_new, "pos_new", (B, T), i32, dev)
+        _want(status, "status", (1,), i32, dev)
+        strides = _strides(k_new, v_new)
     if rows is not None:
-        _want(rows, "rows", (cfg.B, cfg.Hkv, T), torch.int32, dev)
+        _want(rows, "rows", (B, Hkv, T), i32, dev)
     if mass is not None:
-        _want(mass, "mass", (cfg.B, cfg.Hkv, cfg.capacity), torch.float32, dev)
-    _launch(dev, stream, lambda s: _lib.pbsa_kv4_append(
-        _cfg(cfg), ctypes.byref(cache), _ptr(k_new), _ptr(v_new), _strides(k_new, v_new), T,
-        _ptr(pos_new), _ptr(rows), _ptr(mass), _ptr(status), s))
+        _want(mass, "mass", (B, Hkv, cfg.capacity), torch.float32, dev)
+    _launch(i, stream, _lib.pbsa_kv4_append, _cfg(cfg), ctypes.byref(cache), k_new.data_ptr(),
+            v_new.data_ptr(), strides, T, pos_new.data_ptr(), _ptr(rows), _ptr(mass), _ptr(status))
 
 
 def pbsa_kv4_read(cfg, cache, rows, k_out, v_out, status, stream=None):
     """The values of the given rows (None: the first k_out.shape[2] rows)."""
-    dev = _kv4_check(cfg, cache, status)
-    n = k_out.shape[2]
-    _want(k_out, "k_out", (cfg.B, cfg.Hkv, n, cfg.D), _TORCH.get(cfg.dtype), dev)
-    _want(v_out, "v_out", k_out.shape, k_out.dtype, dev)
+    dev, i = _kv4_check(cfg, cache)
+    n, dt = k_out.shape[2], _TORCH.get(cfg.dtype)
+    shape = (cfg.B, cfg.Hkv, n, cfg.D)
+    if not (_ok(k_out, shape, dt, i) and _ok(v_out, shape, dt, i) and
+            _ok(status, (1,), torch.int32, i)):
+        _want(k_out, "k_out", shape, dt, dev)
+        _want(v_out, "v_out", shape, dt, dev)
+        _want(status, "status", (1,), torch.int32, dev)
     if rows is not None:
-        _want(rows, "rows", (cfg.B, cfg.Hkv, n), torch.int32, dev)
-    _launch(dev, stream, lambda s: _lib.pbsa_kv4_read(
-        _cfg(cfg), ctypes.byref(cache), _ptr(rows), n, _ptr(k_out), _ptr(v_out),
-        _ptr(status), s))
+        _want(rows, "rows", shape[:3], torch.int32, dev)
+    _launch(i, stream, _lib.pbsa_kv4_read, _cfg(cfg), ctypes.byref(cache), _ptr(rows), n,
+            _ptr(k_out), v_out.data_ptr(), _ptr(status))
 
 
 def pbsa_kv4_attn(cfg, cache, q, q_pos, kv_len, out, lse, mass, workspace, status, stream=None):
     """Attention of q [B, T, Hq, D] over the cache; q_pos and mass may be None."""
-    dev = _kv4_check(cfg, cache, status)
-    T = q.shape[1]
-    _want(q, "q", (cfg.B, T, cfg.Hq, cfg.D), _TORCH.get(cfg.dtype), dev, True)
-    _want(out, "out", q.shape, q.dtype, dev)
-    _want(lse, "lse", (cfg.B, cfg.Hq, T), torch.float32, dev)
-    _want(kv_len, "kv_len", (cfg.B,), torch.int32, dev)
+    dev, i = _kv4_check(cfg, cache)
+    B, Hq, T, dt = cfg.B, cfg.Hq, q.shape[1], _TORCH.get(cfg.dtype)
+    f32, i32, strides, shape = torch.float32, torch.int32, None, (B, T, Hq, cfg.D)
+    if not (_ok(q, shape, dt, i) and _ok(out, shape, dt, i) and _ok(lse, (B, Hq, T), f32, i) and
+            _ok(kv_len, (B,), i32, i) and _ok(status, (1,), i32, i)):
+        _want(q, "q", shape, dt, dev, True)
+        _want(out, "out", shape, dt, dev)
+        _want(lse, "lse", (B, Hq, T), f32, dev)
+        _want(kv_len, "kv_len", (B,), i32, dev)
+        _want(status, "status", (1,), i32, dev)
+        strides = _strides(q)
     if q_pos is not None:
-        _want(q_pos, "q_pos", (cfg.B, T), torch.int32, dev)
+        _want(q_pos, "q_pos", (B, T), i32, dev)
     if mass is not None:
-        _want(mass, "mass", (cfg.B, cfg.Hkv, cfg.capacity), torch.float32, dev)
+        _want(mass, "mass", (B, cfg.Hkv, cfg.capacity), f32, dev)
     _want_workspace(workspace, dev)
-    _launch(dev, stream, lambda s: _lib.pbsa_kv4_attn(
-        _cfg(cfg), ctypes.byref(cache), _ptr(q), _strides(q), T, _ptr(q_pos), _ptr(kv_len),
-        _ptr(out), _ptr(lse), _ptr(mass), _ptr(workspace), _bytes(workspace), _ptr(status), s))
+    _launch(i, stream, _lib.pbsa_kv4_attn, _cfg(cfg), ctypes.byref(cache), q.data_ptr(), strides, T,
+            _ptr(q_pos), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(mass), _ptr(workspace),
+            _bytes(workspace), _ptr(status))
 
 
 def pbsa_kv4_evict(cfg, pos, mass, n_sink, keep_from, rows, status, stream=None):
     """Chooses rows.shape[2] rows of every sequence and key head for the next tokens."""
-    dev = pos.device
-    shape = (cfg.B, cfg.Hkv, cfg.capacity)
-    _want(pos, "pos", shape, torch.int32, dev)
-    _want(mass, "mass", shape, torch.float32, dev)
-    n = rows.shape[2]
-    _want(rows, "rows", (cfg.B, cfg.Hkv, n), torch.int32, dev)
+    i, n, i32 = pos.get_device(), rows.shape[2], torch.int32
+    B, Hkv = cfg.B, cfg.Hkv
+    shape = (B, Hkv, cfg.capacity)
+    if not (_ok(pos, shape, i32, i) and _ok(mass, shape, torch.float32, i) and
+            _ok(rows, (B, Hkv, n), i32, i) and _ok(status, (1,), i32, i)):
+        dev = pos.device
+        _want(pos, "pos", shape, i32, dev)
+        _want(mass, "mass", shape, torch.float32, dev)
+        _want(rows, "rows", (B, Hkv, n), i32, dev)
+        _want(status, "status", (1,), i32, dev)
     if keep_from is not None:
-        _want(keep_from, "keep_from", (cfg.B,), torch.int32, dev)
-    _want(status, "status", (1,), torch.int32, dev)
-    _launch(dev, stream, lambda s: _lib.pbsa_kv4_evict(
-        _cfg(cfg), _ptr(pos), _ptr(mass), n, n_sink, _ptr(keep_from), _ptr(rows), _ptr(status), s))
+        _want(keep_from, "keep_from", (B,), i32, pos.device)
+    _launch(i, stream, _lib.pbsa_kv4_evict, _cfg(cfg), _ptr(pos), _ptr(mass), n, n_sink,
+            _ptr(keep_from), _ptr(rows), _ptr(status))

@@ -393,7 +393,7 @@ def test_offsets_past_32_bits(cuda_dev):
 
 # ---------------------------------------------------------------------------- eviction
 @pytest.mark.parametrize("B,Hkv,N", [(1, 1, 64), (2, 3, 192), (1, 2, 1088), (2, 1, 4160), (1, 1, 40000 // 64 * 64),
-                                     (1, 1, 131072)])
+                                     (1, 1, 131072), (5, 8, 9280), (5, 8, 20032), (1, 1, 200064)])
 @pytest.mark.parametrize("kind", ["random", "ties", "zeros", "odd"])
 def test_evicted_rows(cuda_dev, B, Hkv, N, kind):
     g = torch.Generator().manual_seed(N)
