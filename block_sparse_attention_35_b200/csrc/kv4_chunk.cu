@@ -1,6 +1,609 @@
+// kv4_chunk.cu - attention of many query rows over the 4-bit token cache, on the tcgen05
+// tensor cores: a chunk of tokens at once, where the products and not the cache's bytes bound.
+//
+// Three kernels share the cache-side step: a 128-key tile of codes is turned into fp16 (exact:
+// a value has six significant bits) and written to shared memory as a 128-byte-swizzled
+// operand tile, once for 256 query rows (attention) or for all rows (masses).
+//
+//  prep_kernel   the queries in fp16, every row scaled by a power of two, as operand tiles of
+//                128 rows, ready for one bulk copy each.
+//  chunk_kernel  S = Q K^T, online softmax, O += P V for 256 rows a CTA (two sides of 128);
+//                CTAs split the work list as attn_kernel's do and join_kernel joins them.
+//  mass_kernel   S^T = K Q^T with the rows' final lse: a lane of tensor memory is a key, so a
+//                key's mass is a sum along one thread's columns, with one owner and one order.
 #include "kv4_attn.cuh"
+
 namespace pbsa {
-bool chunk_takes(const pbsa_kv4_config& c, int R) { return false; }
-cudaError_t launch_chunk_attn(const AttnArgs& a, cudaStream_t st) { return cudaErrorNotSupported; }
-cudaError_t launch_chunk_mass(const AttnArgs& a, cudaStream_t st) { return cudaErrorNotSupported; }
+
+namespace {
+
+constexpr int kHalf = 16384;   // bytes of 128 rows x 64 channels in fp16: one half of a tile
+
+// Instruction descriptor of kind::f16 with fp16 A/B and fp32 accumulate.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+// 32 channels (16 bytes of codes, two scales) of row `row` as four 16-byte chunks of a tile;
+// quarter q of 32 channels each.
+__device__ __forceinline__ void expand32(uint8_t* tile, int row, int q, const uint4& codes, uint32_t scales) {
+    const uint32_t h = e4m3x2_to_half2((uint16_t)scales);
+    const uint32_t sc[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint8_t* half = tile + (q >> 1) * kHalf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 v;
+        e2m1x8_to_half2x4(w[i], v.x, v.y, v.z, v.w);
+        v.x = hmul2_u32(v.x, sc[i >> 1]), v.y = hmul2_u32(v.y, sc[i >> 1]);
+        v.z = hmul2_u32(v.z, sc[i >> 1]), v.w = hmul2_u32(v.w, sc[i >> 1]);
+        *reinterpret_cast<uint4*>(half + sw128_offset(row, (q & 1) * 4 + i)) = v;
+    }
+}
+
+// One warp per query row; D / 4 lanes hold it, four channels each.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) prep_kernel(AttnArgs a) {
+    constexpr int kLanes = D / 4;
+    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    const int ch4 = threadIdx.x % kLanes, rows = a.tiles128 * 128;
+    grid_dependency_launch();
+    const int bh = (int)(row / rows), r = (int)(row % rows);
+    if (bh >= a.k.c.B * a.k.c.Hkv) return;
+    const int b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv;
+    float f;
+    const uint2 v = scale_query4<D>(a, load_query4<T>(a, b, hkv, r, 4 * ch4), f);
+    uint8_t* tile = a.q_tile + ((size_t)bh * a.tiles128 + r / 128) * (128 * D * 2) + (ch4 / 16) * kHalf;
+    *reinterpret_cast<uint2*>(tile + sw128_offset(r % 128, (ch4 % 16) / 2) + (ch4 & 1) * 8) = v;
+    if (ch4 == 0) a.q_scale[(size_t)bh * rows + r] = f;
+}
+
+// ------------------------------------------------------------------------------ masses
+// A CTA owns 128 keys of a (sequence, key head) and walks all rows, 128 at a time, through two
+// buffers in shared and tensor memory; two groups of four warps take the row tiles in turn.
+// Bound by the exponentials (one a key and row, 16 a clock and SM).
+constexpr int kMassGroupThreads = 320;   // 8 warps that compute, one that loads, one that issues
+
+template <int D>
+__global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnArgs a) {
+    constexpr int kTile = 128 * D * 2;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* sK = sm;
+    uint8_t* sQ = sm + kTile;   // [2][kTile]
+    __shared__ __align__(8) uint64_t s_qfull[2], s_qfree[2], s_full[2], s_free[2], s_drain;
+    __shared__ float4 s_col[2][128];   // factor, -lse, limit of a row; by group of warps
+    __shared__ float s_sum[128];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const int N = a.k.c.capacity, per = (N + 127) / 128, bh = blockIdx.x / per, key0 = (blockIdx.x % per) * 128;
+    const int b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv, len = used_rows(a, b);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (key0 >= len) {
+        grid_dependency_wait();
+        return;
+    }
+    const int tiles = a.tiles128;
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_qfull[i], 1);
+            mbar_init(&s_qfree[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 128);
+        }
+        mbar_init(&s_drain, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc(&s_tmem, 256);
+    int pos = kHidden;   // of this thread's key (compute warps: lane of tensor memory)
+    if (warp < 8) {
+        // two threads to a key, each half of its channels
+        const int key = tid & 127, part = tid >> 7;
+        const size_t row = (size_t)bh * N + key0 + key;
+        const bool here = key0 + key < len;
+        if (here) pos = a.k.cache.pos[row];
+        if (pos < 0) pos = kHidden;
+#pragma unroll
+        for (int q = part * (D / 64); q < (part + 1) * (D / 64); ++q) {
+            uint4 codes = make_uint4(0, 0, 0, 0);
+            uint32_t sc = 0;
+            if (pos != kHidden) {
+                codes = __ldg(reinterpret_cast<const uint4*>(a.k.cache.k_codes + row * (D / 2)) + q);
+                sc = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.k_scales + row * (D / 16)) + q);
+            }
+            expand32(sK, key, q, codes, sc);
+        }
+        fence_proxy_async_smem();
+    }
+    grid_dependency_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const size_t tile0 = (size_t)bh * tiles;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            int t = 0;
+            for (; t < tiles; ++t) {
+                const int s = t & 1;
+                if (t >= 2 && !mbar_wait(&s_qfree[s], ((t >> 1) - 1) & 1, &s_abort, a.k.status)) break;
+                mbar_arrive_expect_tx(&s_qfull[s], kTile);
+                bulk_load(smem_u32(sQ + s * kTile), a.q_tile + (tile0 + t) * kTile, kTile, smem_u32(&s_qfull[s]));
+            }
+            // after a wait that ran out: no copy may still be on its way
+            if (t < tiles)
+                for (int i = max(0, t - 2); i < t; ++i) mbar_wait_drain(&s_qfull[i & 1], (i >> 1) & 1, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        constexpr uint32_t idesc = idesc_f16(128, 128, false);
+        const uint32_t k_lo = sdesc_lo(smem_u32(sK), 16);
+        bool ok = true;
+        for (int t = 0; ok && t < tiles; ++t) {
+            const int s = t & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_qfull[s], (t >> 1) & 1, &s_abort, a.k.status));
+            if (ok && t >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&s_free[s], ((t >> 1) - 1) & 1, &s_abort, a.k.status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t q_lo = sdesc_lo(smem_u32(sQ + s * kTile), 16);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                if (elect_one()) umma_ss(tmem + 128 * s, sdesc_make(k_lo + off), sdesc_make(q_lo + off), idesc, kk > 0);
+                __syncwarp();
+            }
+            if (elect_one()) {
+                umma_commit(&s_full[s]);
+                umma_commit(&s_qfree[s]);
+            }
+            __syncwarp();
+        }
+        if (!ok) {   // the products already issued end before tensor memory is released
+            if (elect_one()) umma_commit(&s_drain);
+            __syncwarp();
+            mbar_wait_drain(&s_drain, 0, 100000000ull);
+        }
+    } else {
+        const int group = warp >> 2, key = tid & 127;
+        const uint32_t addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * group;
+        float sum = 0.f;
+        bool ok = true;
+        // a row's column: its factor, lse and limit; thread i prepares column i of the next tile
+        auto column = [&](int t) -> float4 {
+            const int r = t * 128 + key;
+            float lse = INFINITY;
+            if (t < tiles && r < a.R) {
+                const int tt = r / a.G;
+                lse = a.k.lse[((size_t)b * a.k.c.Hq + hkv * a.G + r - tt * a.G) * a.k.T + tt] * kLog2e;
+                if (lse == -INFINITY) lse = INFINITY;   // a row that sees nothing adds nothing
+            }
+            return make_float4(t < tiles ? a.q_scale[(tile0 + t) * 128 + key] : 0.f, -lse,
+                               __int_as_float(row_limit(a, b, r)), 0.f);
+        };
+        float4 next = column(group);
+        for (int t = group; t < tiles; t += 2) {
+            named_bar_sync(1 + group, 128);   // the last tile's columns have been read
+            s_col[group][key] = next;
+            named_bar_sync(1 + group, 128);
+            next = column(t + 2);
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status));
+            if (ok) {
+                tc_fence_after();
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(addr + 32 * c, v);
+                    tmem_ld_wait();
+                    if (c == 3) {
+                        tc_fence_before();
+                        mbar_arrive(&s_free[group]);
+                    }
+                    if (a.k.q_pos) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float4 col = s_col[group][32 * c + e];
+                            const float x = ex2(fmaf(__uint_as_float(v[e]), col.x, col.y));
+                            part[e & 3] += pos <= __float_as_int(col.z) ? x : 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float2 col = *reinterpret_cast<const float2*>(&s_col[group][32 * c + e]);
+                            part[e & 3] += ex2(fmaf(__uint_as_float(v[e]), col.x, col.y));
+                        }
+                    }
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+            }
+        }
+        if (group == 1) s_sum[key] = sum;
+        named_bar_sync(3, 256);
+        if (group == 0 && ok && pos != kHidden) a.k.mass[(size_t)bh * N + key0 + key] += sum + s_sum[key];
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+// --------------------------------------------------------------------------- attention
+// A CTA (one per SM) goes through its run of the work list in segments of one (sequence, key
+// head, group of 256 rows).  Warps 0-3 and 4-7 are the softmax of the two sides (one row a
+// thread), 8-11 expand the cache (one key a thread), 12 issues the products.  Per 128-key tile
+// t the tensor pipe runs PV_A(t-1), QK_A(t), PV_B(t-1), QK_B(t): while one side's softmax
+// works, the pipe has the other side's products.  Tensor memory: S_A | S_B | O_A | O_B, 128
+// columns each; P (fp16) goes over the first half of its own S and is the A operand of PV.
+constexpr int kChunkThreads = 13 * 32;
+constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
+
+struct TileInfo {
+    float bias[128];     // 0, or -infinity for a row that holds no token
+    int pos[128];        // position, or kHidden
+    uint32_t live[4];    // by 32 keys: which hold a token
+    int newest[4];       // by 32 keys: largest position
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
+    constexpr int kTile = 128 * D * 2, kQuarters = D / 32;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* sQ = sm;                  // [2 sides][kTile]
+    uint8_t* sK = sQ + 2 * kTile;      // [2][kTile]
+    uint8_t* sV = sK + 2 * kTile;      // [2][kTile]
+    TileInfo* info = reinterpret_cast<TileInfo*>(sV + 2 * kTile);   // [kInfo]
+    __shared__ __align__(8) uint64_t s_q, s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2];
+    __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_pv[2], s_drain;   // by side
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int N = a.k.c.capacity;
+    grid_dependency_launch();
+    const WorkList list(a, lane);
+    if (blockIdx.x >= list.n) {
+        grid_dependency_wait();
+        return;
+    }
+    if (tid == 0) {
+        s_abort = 0;
+        mbar_init(&s_q, 1);
+        mbar_init(&s_drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_kfull[i], 128);
+            mbar_init(&s_vfull[i], 128);
+            mbar_init(&s_kfree[i], 1);
+            mbar_init(&s_vfree[i], 1);
+            mbar_init(&s_sfull[i], 1);
+            mbar_init(&s_pfull[i], 128);
+            mbar_init(&s_pv[i], 1);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 12) tmem_alloc(&s_tmem, 512);
+    const int w0 = list.first_of(blockIdx.x), total = list.first_of(blockIdx.x + 1) - w0;
+    int b0, before;
+    list.find(a, lane, w0, b0, before);
+    Cursor at;
+    at.start(a, b0, w0 - before);
+    grid_dependency_wait();   // the queries' tiles
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, &s_abort, a.k.status));
+    };
+
+    int seg = 0;
+    uint32_t tile = 0;          // tiles so far
+    uint32_t n_side[2] = {0, 0};   // tiles so far of a side (the second rests in a group of at most 128 rows)
+    for (int left = total; left > 0; ++seg) {
+        const int b = at.b, hkv = at.h / a.groups, grp = at.h - hkv * a.groups, len = at.len, blk0 = at.blk;
+        const int bh = b * a.k.c.Hkv + hkv, row0 = grp * kChunkRows;
+        const int nblk = blocks_of(a, len), tiles = min(nblk - blk0, left);
+        const int sides = row0 + 128 < a.R ? 2 : 1;
+
+        if (warp == 12) {
+            // ------------------------------------------------- queries, and the products
+            constexpr uint32_t idesc_qk = idesc_f16(128, 128, false), idesc_pv = idesc_f16(128, D, true);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&s_q, sides * kTile);
+                for (int x = 0; x < sides; ++x)
+                    bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)bh * a.tiles128 + row0 / 128 + x) * kTile,
+                              kTile, smem_u32(&s_q));
+            }
+            __syncwarp();
+            const bool q_here = wait(&s_q, seg & 1);
+            ok = ok && q_here;
+            auto pv = [&](int x, uint32_t t, bool fresh) {   // P V of tile t
+                const int st = t & 1;
+                ok = ok && wait(&s_pfull[x], n_side[x] & 1) && wait(&s_vfull[st], (t >> 1) & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t v_lo = sdesc_lo(smem_u32(sV + st * kTile), kHalf);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    if (elect_one())
+                        umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, sdesc_make(v_lo + kk * 128), idesc_pv,
+                                (!fresh || kk > 0) ? 1u : 0u);
+                    __syncwarp();
+                }
+                if (elect_one()) {
+                    umma_commit(&s_pv[x]);
+                    if (x == sides - 1) umma_commit(&s_vfree[st]);
+                }
+                __syncwarp();
+                ++n_side[x];
+            };
+            for (int i = 0; ok && i < tiles; ++i) {
+                const uint32_t t = tile + i;
+                const int st = t & 1;
+                ok = wait(&s_kfull[st], (t >> 1) & 1);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= sides) continue;
+                    if (ok && i > 0) pv(x, t - 1, i == 1);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    const uint32_t q_lo = sdesc_lo(smem_u32(sQ + x * kTile), 16), k_lo = sdesc_lo(smem_u32(sK + st * kTile), 16);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        if (elect_one()) umma_ss(tmem + 128 * x, sdesc_make(q_lo + off), sdesc_make(k_lo + off), idesc_qk, kk > 0);
+                        __syncwarp();
+                    }
+                    if (elect_one()) umma_commit(&s_sfull[x]);
+                    __syncwarp();
+                }
+                if (ok) {
+                    if (elect_one()) umma_commit(&s_kfree[st]);
+                    __syncwarp();
+                }
+            }
+            for (int x = 0; x < sides; ++x)
+                if (ok) pv(x, tile + tiles - 1, tiles == 1);
+        } else if (warp >= 8) {
+            // -------------------------------------------------- the cache, into operands
+            const int key = tid - 256;
+            uint4 kc[kQuarters], vc[kQuarters];
+            uint32_t ks[kQuarters], vs[kQuarters];
+            int pos;
+            auto load = [&](int blk) {
+                const int j = blk * 128 + key;
+                const size_t row = (size_t)bh * N + j;
+                pos = j < len ? __ldg(a.k.cache.pos + row) : -1;
+#pragma unroll
+                for (int q = 0; q < kQuarters; ++q) {
+                    kc[q] = vc[q] = make_uint4(0, 0, 0, 0);
+                    ks[q] = vs[q] = 0;
+                }
+                if (j < len) {
+#pragma unroll
+                    for (int q = 0; q < kQuarters; ++q) {
+                        kc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.k_codes + row * (D / 2)) + q);
+                        vc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.v_codes + row * (D / 2)) + q);
+                        ks[q] = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.k_scales + row * (D / 16)) + q);
+                        vs[q] = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.v_scales + row * (D / 16)) + q);
+                    }
+                }
+            };
+            load(blk0);
+            for (int i = 0; i < tiles; ++i) {
+                const uint32_t t = tile + i;
+                const int st = t & 1;
+                const bool here = pos >= 0;
+                if (ok && t >= 2) ok = wait(&s_kfree[st], ((t >> 1) - 1) & 1);
+                if (!ok) break;
+                TileInfo& inf = info[t % kInfo];
+                inf.bias[key] = here ? 0.f : -INFINITY;
+                inf.pos[key] = here ? pos : kHidden;
+                const unsigned live = __ballot_sync(0xffffffffu, here);
+                const int newest = __reduce_max_sync(0xffffffffu, here ? pos : -1);
+                if (lane == 0) {
+                    inf.live[key >> 5] = live;
+                    inf.newest[key >> 5] = newest;
+                }
+#pragma unroll
+                for (int q = 0; q < kQuarters; ++q) expand32(sK + st * kTile, key, q, kc[q], here ? ks[q] : 0u);
+                fence_proxy_async_smem();
+                mbar_arrive(&s_kfull[st]);
+                if (t >= 2) ok = wait(&s_vfree[st], ((t >> 1) - 1) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < kQuarters; ++q) expand32(sV + st * kTile, key, q, vc[q], here ? vs[q] : 0u);
+                fence_proxy_async_smem();
+                mbar_arrive(&s_vfull[st]);
+                if (i + 1 < tiles) load(blk0 + i + 1);
+            }
+        } else if ((warp >> 2) < sides) {
+            // ------------------------------------------------------------------- softmax
+            const int x = warp >> 2, r = row0 + tid;
+            const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const uint32_t s_at = tmem + lane_at + 128 * x, o_at = tmem + lane_at + 256 + 128 * x;
+            const float fac = a.q_scale[((size_t)bh * a.tiles128) * 128 + r];
+            const int lim = row_limit(a, b, r);
+            float mref = -INFINITY, l = 0.f;
+            for (int i = 0; ok && i < tiles; ++i) {
+                const uint32_t n = n_side[x] + i;
+                ok = wait(&s_sfull[x], n & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const TileInfo& inf = info[(tile + i) % kInfo];
+                const int newest = max(max(inf.newest[0], inf.newest[1]), max(inf.newest[2], inf.newest[3]));
+                // some row of this warp may not see some token of the tile (rows past the last
+                // are never read back)
+                const bool causal = __any_sync(0xffffffffu, r < a.R && newest > lim);
+                // 32 products, with -infinity for what the row does not see
+                auto load32 = [&](int c, float (&v)[32]) {
+                    uint32_t u[32];
+                    tmem_ld32(s_at + 32 * c, u);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[e]);
+                    if (causal) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const int4 p = *reinterpret_cast<const int4*>(&inf.pos[32 * c + e]);
+                            v[e] = p.x <= lim ? v[e] : -INFINITY;
+                            v[e + 1] = p.y <= lim ? v[e + 1] : -INFINITY;
+                            v[e + 2] = p.z <= lim ? v[e + 2] : -INFINITY;
+                            v[e + 3] = p.w <= lim ? v[e + 3] : -INFINITY;
+                        }
+                    } else if (inf.live[c] != 0xffffffffu) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 p = *reinterpret_cast<const float4*>(&inf.bias[32 * c + e]);
+                            v[e] += p.x, v[e + 1] += p.y, v[e + 2] += p.z, v[e + 3] += p.w;
+                        }
+                    }
+                };
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    load32(c, v);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(v[e], v[e + 1]));
+                }
+                const float mn = top * fac - kShift;
+                const bool grow = mn > mref + kLag;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float k = grow ? ex2(mref - mn) : 1.f;   // 0 from the initial -inf
+                    if (i > 0) {
+                        ok = wait(&s_pv[x], (n - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32(o_at + 32 * c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * k);
+                            tmem_st32(o_at + 32 * c, v);
+                        }
+                        tmem_st_wait();
+                    }
+                    if (grow) {
+                        l *= k;
+                        mref = mn;
+                    }
+                }
+                const float ref = mref == -INFINITY ? 0.f : -mref;   // none seen so far: 2^-inf
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    load32(c, v);
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float y = ex2(fmaf(v[2 * e], fac, ref)), z = ex2(fmaf(v[2 * e + 1], fac, ref));
+                        part[(2 * e) & 3] += y;
+                        part[(2 * e + 1) & 3] += z;
+                        const __half2 h = __floats2half2_rn(y, z);
+                        p[e] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    tmem_st16(s_at + 16 * c, p);   // over products that have been read
+                }
+                l += (part[0] + part[1]) + (part[2] + part[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&s_pfull[x]);
+            }
+            if (ok) ok = wait(&s_pv[x], (n_side[x] + tiles - 1) & 1);
+            if (ok) {
+                tc_fence_after();
+                const bool whole = blk0 == 0 && tiles == nblk;
+                const size_t slot = ((size_t)blockIdx.x * 2 + (blk0 == 0)) * kChunkRows + tid;
+                const int tt = r / a.G, h = hkv * a.G + r - tt * a.G;
+                T* out = static_cast<T*>(a.k.out) + (((size_t)b * a.k.T + tt) * a.k.c.Hq + h) * D;
+                const float inv = l == 0.f ? 0.f : a.k.c.v_unit / l;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(o_at + 32 * c, v);
+                    tmem_ld_wait();
+                    if (r < a.R) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float4 y = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                   __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                            if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (whole) store4(out + 32 * c + e, y, inv);
+                            else *reinterpret_cast<float4*>(a.part_o + slot * D + 32 * c + e) = y;
+                        }
+                    }
+                }
+                if (r < a.R) {
+                    if (whole)
+                        a.k.lse[((size_t)b * a.k.c.Hq + h) * a.k.T + tt] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
+                    else
+                        a.part_ml[slot] = make_float2(mref, l);
+                }
+            }
+        }
+        tile += tiles;
+        if (warp != 12)
+            for (int x = 0; x < sides; ++x) n_side[x] += tiles;
+        left -= tiles;
+        if (left > 0) {
+            at.blk = blk0 + tiles - 1;
+            at.next(a, left);
+        }
+        tc_fence_before();
+        __syncthreads();   // the segment's operands and sums have been read
+        tc_fence_after();
+    }
+    if (warp == 12) {
+        if (!ok) {   // the products already issued end before tensor memory is released
+            if (elect_one()) umma_commit(&s_drain);
+            __syncwarp();
+            mbar_wait_drain(&s_drain, 0, 100000000ull);
+        }
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+bool chunk_takes(const pbsa_kv4_config& c, int R) { return R > 64; }
+
+cudaError_t launch_chunk_attn(const AttnArgs& a, cudaStream_t st) {
+    auto run = [&](auto prep, auto kernel, int D) -> cudaError_t {
+        const long long threads = (long long)a.k.c.B * a.k.c.Hkv * a.tiles128 * 128 * (D / 4);
+        prep<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        const size_t smem = 6 * 128 * D * 2 + kInfo * sizeof(TileInfo) + 1024;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        return launch_after(kernel, dim3((unsigned)a.ctas), kChunkThreads, smem, st, a);
+    };
+    const bool bf16 = a.k.c.dtype == PBSA_DTYPE_BF16;
+    if (a.k.c.D == 64)
+        return bf16 ? run(prep_kernel<64, __nv_bfloat16>, chunk_kernel<64, __nv_bfloat16>, 64)
+                    : run(prep_kernel<64, __half>, chunk_kernel<64, __half>, 64);
+    return bf16 ? run(prep_kernel<128, __nv_bfloat16>, chunk_kernel<128, __nv_bfloat16>, 128)
+                : run(prep_kernel<128, __half>, chunk_kernel<128, __half>, 128);
+}
+
+cudaError_t launch_chunk_mass(const AttnArgs& a, cudaStream_t st) {
+    auto run = [&](auto kernel, int D) -> cudaError_t {
+        const int smem = 3 * 128 * D * 2 + 1024;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        const dim3 grid((unsigned)(a.k.c.B * a.k.c.Hkv * ((a.k.c.capacity + 127) / 128)));
+        return launch_after(kernel, grid, kMassGroupThreads, (size_t)smem, st, a);
+    };
+    return a.k.c.D == 64 ? run(chunk_mass_kernel<64>, 64) : run(chunk_mass_kernel<128>, 128);
+}
+
+}  // namespace pbsa

@@ -217,6 +217,48 @@ def test_rows_of_every_count(cuda_dev, D, dtype, Hq, Hkv, T):
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16), (128, torch.float16)])
+@pytest.mark.parametrize("Hq,Hkv,T", [(1, 1, 65), (2, 1, 64), (3, 1, 43), (8, 2, 65), (1, 1, 300), (4, 2, 257)])
+@pytest.mark.parametrize("N,lens", [(64, [64, 33]), (448, [448, 129])])
+def test_chunks(cuda_dev, D, dtype, Hq, Hkv, T, N, lens):
+    """65 to 514 query rows to a key head: one side of 128 and two, ragged groups, several
+    segments a CTA and several CTAs a segment."""
+    c = Cache(cuda_dev, B=2, Hq=Hq, Hkv=Hkv, D=D, N=N, dtype=dtype, seed=T + Hq)
+    c.pos[torch.rand(c.pos.shape, generator=c.g).to(cuda_dev) < 0.05] = -1
+    q = c.queries(T)
+    mass = c.mass.clone()
+    out, lse = c.attend(q, None, c.i32(lens), mass)
+    check_attention(c, q, None, lens, out, lse, mass, c.mass)
+    q_pos = torch.randint(0, 2 * N, (2, T), generator=c.g, dtype=torch.int32).to(cuda_dev)
+    q_pos[1, -3:] = -1                                   # padded places
+    q_pos[0, :40] = 2                                    # rows that see next to nothing
+    mass = c.mass.clone()
+    out, lse = c.attend(q, q_pos, c.i32(lens), mass)
+    check_attention(c, q, q_pos, lens, out, lse, mass, c.mass)
+    again = c.mass.clone()
+    out2, lse2 = c.attend(q, q_pos, c.i32(lens), again)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and torch.equal(mass, again)
+    assert int(c.status.item()) == 0
+
+
+def test_chunk_of_a_long_cache(cuda_dev):
+    """Parts of one head on many CTAs, an empty sequence and garbage in rows without a token."""
+    c = Cache(cuda_dev, B=3, Hq=2, Hkv=1, D=128, N=4096, seed=21)
+    c.pos[torch.rand(c.pos.shape, generator=c.g).to(cuda_dev) < 0.02] = -1
+    lens = [4096, 0, 1500]
+    gone = (c.pos < 0) | (torch.arange(4096, device=cuda_dev) >= c.i32(lens)[:, None, None])
+    q = c.queries(70, 2.0)
+    mass = c.mass.clone()
+    out, lse = c.attend(q, None, c.i32(lens), mass)
+    k, v = c.values()
+    check_attention(c, q, None, lens, out, lse, mass, c.mass, k=k, v=v)
+    for t, x in ((c.kc, 255), (c.ks, 127), (c.vc, 255), (c.vs, 127)):
+        t[gone] = x
+    again = c.mass.clone()
+    out2, lse2 = c.attend(q, None, c.i32(lens), again)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and torch.equal(mass, again)
+
+
 @pytest.mark.parametrize("N,lens", [(64, [0, 1, 2, 15]), (64, [16, 17, 63, 64]), (1088, [1088, 1073, 257, 0]),
                                     (4096, [4096, 1, 2049, 0])])
 @pytest.mark.parametrize("G", [1, 10])
