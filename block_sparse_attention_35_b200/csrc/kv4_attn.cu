@@ -435,36 +435,45 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
 }
 
 // Joins the segments of heads whose keys were shared by several CTAs, and writes the heads
-// that have no keys.  One CTA per row: D / 4 lanes hold its channels, PARTS of them in
-// parallel take the parts in turn (a long cache of one head has a part per CTA of the GPU).
-// It is launched while attn_kernel still runs and waits for it before it reads its parts.
+// that have no keys.  D / 4 lanes hold a row's channels, PARTS of them in parallel take its
+// parts in turn (a long cache of one head has a part per CTA of the GPU).  It is launched while
+// the kernel before it still runs and waits for that one before it reads its parts.
+template <int D, int PARTS>
+constexpr int kJoinThreads = PARTS * D / 4 > 256 ? PARTS * D / 4 : 256;
+
 template <int D, int PARTS, typename T>
-__global__ void __launch_bounds__(PARTS * D / 4) join_kernel(AttnArgs a) {
-    constexpr int kLanes = D / 4;
-    __shared__ float4 s_v[PARTS][kLanes];
-    __shared__ float s_m[PARTS], s_l[PARTS];
-    const int lane = threadIdx.x & 31, bh = blockIdx.x / a.R, qrow = blockIdx.x % a.R;
+__global__ void __launch_bounds__(kJoinThreads<D, PARTS>) join_kernel(AttnArgs a) {
+    constexpr int kLanes = D / 4, kRows = kJoinThreads<D, PARTS> / (PARTS * kLanes);
+    __shared__ float4 s_v[kRows][PARTS][kLanes];
+    __shared__ float s_m[kRows][PARTS], s_l[kRows][PARTS];
+    const int lane = threadIdx.x & 31, mine = threadIdx.x / (PARTS * kLanes);
+    const long long row = (long long)blockIdx.x * kRows + mine;
+    const bool valid = row < (long long)a.k.c.B * a.k.c.Hkv * a.R;
+    const int bh = valid ? (int)(row / a.R) : 0, qrow = valid ? (int)(row % a.R) : 0;
     const int b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv;
-    const int d = (threadIdx.x % kLanes) * 4, part = threadIdx.x / kLanes;
+    const int d = (threadIdx.x % kLanes) * 4, part = threadIdx.x / kLanes % PARTS;
     const WorkList list(a, lane);
-    const int n = blocks_of(a, used_rows(a, b));
+    const int n = valid ? blocks_of(a, used_rows(a, b)) : 0;
     int first = 0, last = 0;
+    // rows of one warp may be of two sequences (D = 64): the lanes ask together, for each
+    const int before_lo = list.before(a, lane, __shfl_sync(0xffffffffu, b, 0));
+    const int before_hi = list.before(a, lane, __shfl_sync(0xffffffffu, b, 31));
     if (n > 0) {
-        const int w0 = list.before(a, lane, b) + (hkv * a.groups + qrow / a.rows) * n;
+        const int w0 = (lane < kLanes ? before_lo : before_hi) + (hkv * a.groups + qrow / a.rows) * n;
         first = list.cta_of(w0);
         last = list.cta_of(w0 + n - 1);
     }
     if (blockIdx.x == 0)
-        for (int x = threadIdx.x; x < a.k.c.B; x += PARTS * kLanes)
+        for (int x = threadIdx.x; x < a.k.c.B; x += kJoinThreads<D, PARTS>)
             if (a.k.kv_len[x] != used_rows(a, x)) set_status(a.k.status, PBSA_ERR_DEVICE_CHECK);
     grid_dependency_wait();
     grid_dependency_launch();
-    if (n > 0 && first == last) return;   // written by its CTA
+    const bool split = valid && !(n > 0 && first == last);   // else written by its CTA, or no row
     // the first CTA's part is its last segment (slot 1), the others' their first (slot 0)
-    const size_t base = qrow % a.rows;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float mx = -INFINITY, sum = 0.f;
-    if (n > 0) {
+    if (split && n > 0) {
+        const size_t base = qrow % a.rows;
 #pragma unroll 4
         for (int i = first + part; i <= last; i += PARTS) {
             const size_t at = base + ((size_t)2 * i + (i == first)) * a.rows;
@@ -477,25 +486,28 @@ __global__ void __launch_bounds__(PARTS * D / 4) join_kernel(AttnArgs a) {
             mx = mn;
         }
     }
-    s_v[part][threadIdx.x % kLanes] = v;
-    if (d == 0) {
-        s_m[part] = mx;
-        s_l[part] = sum;
-    }
-    __syncthreads();
-    if (part > 0) return;
-    for (int i = 1; i < PARTS; ++i) mx = fmaxf(mx, s_m[i]);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    v = make_float4(0.f, 0.f, 0.f, 0.f);
-    sum = 0.f;
+    if (PARTS > 1) {
+        s_v[mine][part][threadIdx.x % kLanes] = v;
+        if (d == 0) {
+            s_m[mine][part] = mx;
+            s_l[mine][part] = sum;
+        }
+        __syncthreads();
+        if (part == 0) {
+            for (int i = 1; i < PARTS; ++i) mx = fmaxf(mx, s_m[mine][i]);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+            sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-        const float k = ex2(s_m[i] - ref);
-        const float4 x = s_v[i][threadIdx.x];
-        v.x += k * x.x, v.y += k * x.y, v.z += k * x.z, v.w += k * x.w;
-        sum += k * s_l[i];
+            for (int i = 0; i < PARTS; ++i) {
+                const float k = ex2(s_m[mine][i] - ref);
+                const float4 x = s_v[mine][i][threadIdx.x % kLanes];
+                v.x += k * x.x, v.y += k * x.y, v.z += k * x.z, v.w += k * x.w;
+                sum += k * s_l[mine][i];
+            }
+        }
     }
-    finish_row<D, T>(a, b, hkv, qrow, d, v, mx, sum);
+    if (split && part == 0) finish_row<D, T>(a, b, hkv, qrow, d, v, mx, sum);
 }
 
 // Masses from the kept logits of at most eight rows: a thread takes four cached rows.
@@ -650,10 +662,16 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
     else e = run_rows<D, 4, T, false>(a, st);
     if (e != cudaSuccess) return e;
     const int bh = a.k.c.B * a.k.c.Hkv;
+    const long long rows = (long long)bh * a.R;
+    auto join = [&](auto kernel, int threads, int parts) {
+        const int per = threads / (parts * D / 4);
+        return launch_after(kernel, dim3((unsigned)((rows + per - 1) / per)), threads, 0, st, a);
+    };
     // few heads have many parts each
-    const dim3 rows((unsigned)(bh * a.R));
-    if (a.ctas >= 8 * a.k.c.B * a.heads) e = launch_after(join_kernel<D, 16, T>, rows, 16 * D / 4, 0, st, a);
-    else e = launch_after(join_kernel<D, 4, T>, rows, 4 * D / 4, 0, st, a);
+    const int parts = a.ctas / (a.k.c.B * a.heads);
+    if (parts >= 8) e = join(join_kernel<D, 16, T>, kJoinThreads<D, 16>, 16);
+    else if (parts >= 2) e = join(join_kernel<D, 4, T>, kJoinThreads<D, 4>, 4);
+    else e = join(join_kernel<D, 1, T>, kJoinThreads<D, 1>, 1);
     if (e != cudaSuccess || !a.k.mass) return e;
     if (chunk) return launch_chunk_mass(a, st);
     if (keeps_logits(a.R)) {

@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
     uint8_t* sK = sm;
     uint8_t* sQ = sm + kTile;   // [2][kTile]
     __shared__ __align__(8) uint64_t s_qfull[2], s_qfree[2], s_full[2], s_free[2], s_drain;
-    __shared__ float4 s_col[2][128];   // factor, -lse, limit of a row; by group of warps
+    __shared__ __align__(16) float2 s_col[2][2][128];   // factor and -lse of a row; by group of warps, tile
+    __shared__ int s_lim[2][2][128];
     __shared__ float s_sum[128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -185,36 +186,38 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
         };
         float4 next = column(group);
         for (int t = group; t < tiles; t += 2) {
-            named_bar_sync(1 + group, 128);   // the last tile's columns have been read
-            s_col[group][key] = next;
-            named_bar_sync(1 + group, 128);
+            const int buf = (t >> 1) & 1;
+            s_col[group][buf][key] = make_float2(next.x, next.y);
+            s_lim[group][buf][key] = __float_as_int(next.z);
+            named_bar_sync(1 + group, 128);   // and the columns two tiles back have been read
             next = column(t + 2);
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status));
             if (ok) {
                 tc_fence_after();
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t u[2][16];
+                tmem_ld16(addr, u[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(addr + 32 * c, v);
+                for (int c = 0; c < 8; ++c) {
                     tmem_ld_wait();
-                    if (c == 3) {
+                    if (c < 7) {
+                        tmem_ld16(addr + 16 * (c + 1), u[(c + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         mbar_arrive(&s_free[group]);
                     }
-                    if (a.k.q_pos) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float4 col = s_col[group][32 * c + e];
-                            const float x = ex2(fmaf(__uint_as_float(v[e]), col.x, col.y));
-                            part[e & 3] += pos <= __float_as_int(col.z) ? x : 0.f;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 col = *reinterpret_cast<const float4*>(&s_col[group][buf][16 * c + e]);
+                        float x = ex2(fmaf(__uint_as_float(u[c & 1][e]), col.x, col.y));
+                        float y = ex2(fmaf(__uint_as_float(u[c & 1][e + 1]), col.z, col.w));
+                        if (a.k.q_pos) {
+                            const int2 lim = *reinterpret_cast<const int2*>(&s_lim[group][buf][16 * c + e]);
+                            x = pos <= lim.x ? x : 0.f;
+                            y = pos <= lim.y ? y : 0.f;
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float2 col = *reinterpret_cast<const float2*>(&s_col[group][32 * c + e]);
-                            part[e & 3] += ex2(fmaf(__uint_as_float(v[e]), col.x, col.y));
-                        }
+                        part[e & 3] += x;
+                        part[(e + 1) & 3] += y;
                     }
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
@@ -301,22 +304,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, &s_abort, a.k.status));
     };
 
-    int seg = 0;
-    uint32_t tile = 0;          // tiles so far
-    uint32_t n_side[2] = {0, 0};   // tiles so far of a side (the second rests in a group of at most 128 rows)
-    for (int left = total; left > 0; ++seg) {
-        const int b = at.b, hkv = at.h / a.groups, grp = at.h - hkv * a.groups, len = at.len, blk0 = at.blk;
-        const int bh = b * a.k.c.Hkv + hkv, row0 = grp * kChunkRows;
-        const int nblk = blocks_of(a, len), tiles = min(nblk - blk0, left);
-        const int sides = row0 + 128 < a.R ? 2 : 1;
+    // A segment: what every role needs of it; and the step to the next one.
+    struct Segment {
+        int b, hkv, len, blk0, bh, row0, nblk, tiles, sides;
+    };
+    int left = total;
+    uint32_t tile = 0;             // tiles so far
+    uint32_t n_side[2] = {0, 0};   // of a side (the second rests in a group of at most 128 rows)
+    auto segment = [&]() -> Segment {
+        Segment s;
+        s.b = at.b, s.len = at.len, s.blk0 = at.blk;
+        s.hkv = at.h / a.groups;
+        s.bh = s.b * a.k.c.Hkv + s.hkv;
+        s.row0 = (at.h - s.hkv * a.groups) * kChunkRows;
+        s.nblk = blocks_of(a, s.len);
+        s.tiles = min(s.nblk - s.blk0, left);
+        s.sides = s.row0 + 128 < a.R ? 2 : 1;
+        return s;
+    };
+    auto finish = [&](const Segment& s) {
+        tile += s.tiles;
+        left -= s.tiles;
+        if (left > 0) {
+            at.blk = s.blk0 + s.tiles - 1;
+            at.next(a, left);
+        }
+        tc_fence_before();
+        __syncthreads();   // the segment's operands and sums have been read
+        tc_fence_after();
+    };
 
+    if (warp >= 8) {
         if (warp == 12) {
             // ------------------------------------------------- queries, and the products
+            for (int seg = 0; left > 0; ++seg) {
+                const Segment s = segment();
             constexpr uint32_t idesc_qk = idesc_f16(128, 128, false), idesc_pv = idesc_f16(128, D, true);
             if (elect_one()) {
-                mbar_arrive_expect_tx(&s_q, sides * kTile);
-                for (int x = 0; x < sides; ++x)
-                    bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)bh * a.tiles128 + row0 / 128 + x) * kTile,
+                mbar_arrive_expect_tx(&s_q, s.sides * kTile);
+                for (int x = 0; x < s.sides; ++x)
+                    bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)s.bh * a.tiles128 + s.row0 / 128 + x) * kTile,
                               kTile, smem_u32(&s_q));
             }
             __syncwarp();
@@ -337,18 +364,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 }
                 if (elect_one()) {
                     umma_commit(&s_pv[x]);
-                    if (x == sides - 1) umma_commit(&s_vfree[st]);
+                    if (x == s.sides - 1) umma_commit(&s_vfree[st]);
                 }
                 __syncwarp();
                 ++n_side[x];
             };
-            for (int i = 0; ok && i < tiles; ++i) {
+            for (int i = 0; ok && i < s.tiles; ++i) {
                 const uint32_t t = tile + i;
                 const int st = t & 1;
                 ok = wait(&s_kfull[st], (t >> 1) & 1);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (x >= sides) continue;
+                    if (x >= s.sides) continue;
                     if (ok && i > 0) pv(x, t - 1, i == 1);
                     if (!ok) continue;
                     tc_fence_after();
@@ -367,24 +394,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     __syncwarp();
                 }
             }
-            for (int x = 0; x < sides; ++x)
-                if (ok) pv(x, tile + tiles - 1, tiles == 1);
-        } else if (warp >= 8) {
+            for (int x = 0; x < s.sides; ++x)
+                if (ok) pv(x, tile + s.tiles - 1, s.tiles == 1);
+                finish(s);
+            }
+            if (!ok) {   // the products already issued end before tensor memory is released
+                if (elect_one()) umma_commit(&s_drain);
+                __syncwarp();
+                mbar_wait_drain(&s_drain, 0, 100000000ull);
+            }
+            tmem_dealloc(tmem, 512);
+        } else if (warp < 12) {
             // -------------------------------------------------- the cache, into operands
+            while (left > 0) {
+                const Segment s = segment();
             const int key = tid - 256;
             uint4 kc[kQuarters], vc[kQuarters];
             uint32_t ks[kQuarters], vs[kQuarters];
             int pos;
             auto load = [&](int blk) {
                 const int j = blk * 128 + key;
-                const size_t row = (size_t)bh * N + j;
-                pos = j < len ? __ldg(a.k.cache.pos + row) : -1;
+                const size_t row = (size_t)s.bh * N + j;
+                pos = j < s.len ? __ldg(a.k.cache.pos + row) : -1;
 #pragma unroll
                 for (int q = 0; q < kQuarters; ++q) {
                     kc[q] = vc[q] = make_uint4(0, 0, 0, 0);
                     ks[q] = vs[q] = 0;
                 }
-                if (j < len) {
+                if (j < s.len) {
 #pragma unroll
                     for (int q = 0; q < kQuarters; ++q) {
                         kc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.k_codes + row * (D / 2)) + q);
@@ -394,8 +431,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     }
                 }
             };
-            load(blk0);
-            for (int i = 0; i < tiles; ++i) {
+            load(s.blk0);
+            for (int i = 0; i < s.tiles; ++i) {
                 const uint32_t t = tile + i;
                 const int st = t & 1;
                 const bool here = pos >= 0;
@@ -420,18 +457,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 for (int q = 0; q < kQuarters; ++q) expand32(sV + st * kTile, key, q, vc[q], here ? vs[q] : 0u);
                 fence_proxy_async_smem();
                 mbar_arrive(&s_vfull[st]);
-                if (i + 1 < tiles) load(blk0 + i + 1);
+                if (i + 1 < s.tiles) load(s.blk0 + i + 1);
             }
-        } else if ((warp >> 2) < sides) {
-            // ------------------------------------------------------------------- softmax
-            const int x = warp >> 2, r = row0 + tid;
+                finish(s);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------- softmax
+        const int x = warp >> 2;
+        uint32_t n_mine = 0;   // tiles so far of this side
+        while (left > 0) {
+            const Segment s = segment();
+            if (x < s.sides) {
+            const int r = s.row0 + tid;
             const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const uint32_t s_at = tmem + lane_at + 128 * x, o_at = tmem + lane_at + 256 + 128 * x;
-            const float fac = a.q_scale[((size_t)bh * a.tiles128) * 128 + r];
-            const int lim = row_limit(a, b, r);
+            const float fac = a.q_scale[((size_t)s.bh * a.tiles128) * 128 + r];
+            const int lim = row_limit(a, s.b, r);
             float mref = -INFINITY, l = 0.f;
-            for (int i = 0; ok && i < tiles; ++i) {
-                const uint32_t n = n_side[x] + i;
+            for (int i = 0; ok && i < s.tiles; ++i) {
+                const uint32_t n = n_mine + i;
                 ok = wait(&s_sfull[x], n & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -440,39 +485,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 // some row of this warp may not see some token of the tile (rows past the last
                 // are never read back)
                 const bool causal = __any_sync(0xffffffffu, r < a.R && newest > lim);
-                // 32 products, with -infinity for what the row does not see
-                auto load32 = [&](int c, float (&v)[32]) {
-                    uint32_t u[32];
-                    tmem_ld32(s_at + 32 * c, u);
-                    tmem_ld_wait();
+                // goes over the products, 32 at a time (the next on their way), with
+                // -infinity for what the row does not see
+                auto sweep = [&](auto&& use) {
+                    uint32_t u[2][32];
+                    tmem_ld32(s_at, u[0]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[e]);
-                    if (causal) {
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait();
+                        if (c < 3) tmem_ld32(s_at + 32 * (c + 1), u[(c + 1) & 1]);
+                        float v[32];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const int4 p = *reinterpret_cast<const int4*>(&inf.pos[32 * c + e]);
-                            v[e] = p.x <= lim ? v[e] : -INFINITY;
-                            v[e + 1] = p.y <= lim ? v[e + 1] : -INFINITY;
-                            v[e + 2] = p.z <= lim ? v[e + 2] : -INFINITY;
-                            v[e + 3] = p.w <= lim ? v[e + 3] : -INFINITY;
+                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[c & 1][e]);
+                        if (causal) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const int4 q = *reinterpret_cast<const int4*>(&inf.pos[32 * c + e]);
+                                v[e] = q.x <= lim ? v[e] : -INFINITY;
+                                v[e + 1] = q.y <= lim ? v[e + 1] : -INFINITY;
+                                v[e + 2] = q.z <= lim ? v[e + 2] : -INFINITY;
+                                v[e + 3] = q.w <= lim ? v[e + 3] : -INFINITY;
+                            }
+                        } else if (inf.live[c] != 0xffffffffu) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 q = *reinterpret_cast<const float4*>(&inf.bias[32 * c + e]);
+                                v[e] += q.x, v[e + 1] += q.y, v[e + 2] += q.z, v[e + 3] += q.w;
+                            }
                         }
-                    } else if (inf.live[c] != 0xffffffffu) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 p = *reinterpret_cast<const float4*>(&inf.bias[32 * c + e]);
-                            v[e] += p.x, v[e + 1] += p.y, v[e + 2] += p.z, v[e + 3] += p.w;
-                        }
+                        use(c, v);
                     }
                 };
-                float top = -INFINITY;
+                float top[2] = {-INFINITY, -INFINITY};
+                sweep([&](int, const float (&v)[32]) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    load32(c, v);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(v[e], v[e + 1]));
-                }
-                const float mn = top * fac - kShift;
+                    for (int e = 0; e < 32; e += 4) {
+                        top[0] = fmaxf(top[0], fmaxf(v[e], v[e + 1]));
+                        top[1] = fmaxf(top[1], fmaxf(v[e + 2], v[e + 3]));
+                    }
+                });
+                const float mn = fmaxf(top[0], top[1]) * fac - kShift;
                 const bool grow = mn > mref + kLag;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float k = grow ? ex2(mref - mn) : 1.f;   // 0 from the initial -inf
@@ -498,10 +550,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 }
                 const float ref = mref == -INFINITY ? 0.f : -mref;   // none seen so far: 2^-inf
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    load32(c, v);
+                sweep([&](int c, const float (&v)[32]) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -512,19 +561,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                         p[e] = *reinterpret_cast<const uint32_t*>(&h);
                     }
                     tmem_st16(s_at + 16 * c, p);   // over products that have been read
-                }
+                });
                 l += (part[0] + part[1]) + (part[2] + part[3]);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&s_pfull[x]);
             }
-            if (ok) ok = wait(&s_pv[x], (n_side[x] + tiles - 1) & 1);
+            if (ok) ok = wait(&s_pv[x], (n_mine + s.tiles - 1) & 1);
             if (ok) {
                 tc_fence_after();
-                const bool whole = blk0 == 0 && tiles == nblk;
-                const size_t slot = ((size_t)blockIdx.x * 2 + (blk0 == 0)) * kChunkRows + tid;
-                const int tt = r / a.G, h = hkv * a.G + r - tt * a.G;
-                T* out = static_cast<T*>(a.k.out) + (((size_t)b * a.k.T + tt) * a.k.c.Hq + h) * D;
+                const bool whole = s.blk0 == 0 && s.tiles == s.nblk;
+                const size_t slot = ((size_t)blockIdx.x * 2 + (s.blk0 == 0)) * kChunkRows + tid;
+                const int tt = r / a.G, h = s.hkv * a.G + r - tt * a.G;
+                T* out = static_cast<T*>(a.k.out) + (((size_t)s.b * a.k.T + tt) * a.k.c.Hq + h) * D;
                 const float inv = l == 0.f ? 0.f : a.k.c.v_unit / l;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -544,31 +593,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 }
                 if (r < a.R) {
                     if (whole)
-                        a.k.lse[((size_t)b * a.k.c.Hq + h) * a.k.T + tt] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
+                        a.k.lse[((size_t)s.b * a.k.c.Hq + h) * a.k.T + tt] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
                     else
                         a.part_ml[slot] = make_float2(mref, l);
                 }
             }
+                n_mine += s.tiles;
+            }
+            finish(s);
         }
-        tile += tiles;
-        if (warp != 12)
-            for (int x = 0; x < sides; ++x) n_side[x] += tiles;
-        left -= tiles;
-        if (left > 0) {
-            at.blk = blk0 + tiles - 1;
-            at.next(a, left);
-        }
-        tc_fence_before();
-        __syncthreads();   // the segment's operands and sums have been read
-        tc_fence_after();
-    }
-    if (warp == 12) {
-        if (!ok) {   // the products already issued end before tensor memory is released
-            if (elect_one()) umma_commit(&s_drain);
-            __syncwarp();
-            mbar_wait_drain(&s_drain, 0, 100000000ull);
-        }
-        tmem_dealloc(tmem, 512);
     }
 }
 
