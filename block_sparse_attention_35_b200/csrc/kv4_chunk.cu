@@ -238,10 +238,11 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // --------------------------------------------------------------------------- attention
 // A CTA (one per SM) goes through its run of the work list in segments of one (sequence, key
 // head, group of 256 rows).  Warps 0-3 and 4-7 are the softmax of the two sides (one row a
-// thread), 8-11 expand the cache (one key a thread), 12 issues the products.  Per 128-key tile
-// t the tensor pipe runs PV_A(t-1), QK_A(t), PV_B(t-1), QK_B(t): while one side's softmax
-// works, the pipe has the other side's products.  Tensor memory: S_A | S_B | O_A | O_B, 128
-// columns each; P (fp16) goes over the first half of its own S and is the A operand of PV.
+// thread), 8-11 expand the cache (one key a thread, 128 at a time), 12 issues the products, 64
+// keys at a time: QK of step u + 2 goes right behind PV of step u into the same columns, so that
+// a side's softmax finds its next scores ready when it is done with the last ones.  Tensor
+// memory: two S of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its
+// own S and is the A operand of PV.  One thread's products execute in issue order.
 constexpr int kChunkThreads = 13 * 32;
 constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
 
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     uint8_t* sV = sK + 2 * kTile;      // [2][kTile]
     TileInfo* info = reinterpret_cast<TileInfo*>(sV + 2 * kTile);   // [kInfo]
     __shared__ __align__(8) uint64_t s_q, s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2];
-    __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_pv[2], s_drain;   // by side
+    __shared__ __align__(8) uint64_t s_sfull[2][2], s_pfull[2][2], s_pv[2], s_drain;   // by side, S
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -282,8 +283,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             mbar_init(&s_vfull[i], 128);
             mbar_init(&s_kfree[i], 1);
             mbar_init(&s_vfree[i], 1);
-            mbar_init(&s_sfull[i], 1);
-            mbar_init(&s_pfull[i], 128);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&s_sfull[i][j], 1);
+                mbar_init(&s_pfull[i][j], 128);
+            }
             mbar_init(&s_pv[i], 1);
         }
         fence_barrier_init();
@@ -310,7 +313,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     };
     int left = total;
     uint32_t tile = 0;             // tiles so far
-    uint32_t n_side[2] = {0, 0};   // of a side (the second rests in a group of at most 128 rows)
     auto segment = [&]() -> Segment {
         Segment s;
         s.b = at.b, s.len = at.len, s.blk0 = at.blk;
@@ -337,9 +339,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     if (warp >= 8) {
         if (warp == 12) {
             // ------------------------------------------------- queries, and the products
+            uint32_t n_side[2] = {0, 0};   // tiles so far of a side (the second rests in a group of at most 128 rows)
             for (int seg = 0; left > 0; ++seg) {
                 const Segment s = segment();
-            constexpr uint32_t idesc_qk = idesc_f16(128, 128, false), idesc_pv = idesc_f16(128, D, true);
+            constexpr uint32_t idesc_qk = idesc_f16(128, 64, false), idesc_pv = idesc_f16(128, D, true);
             if (elect_one()) {
                 mbar_arrive_expect_tx(&s_q, s.sides * kTile);
                 for (int x = 0; x < s.sides; ++x)
@@ -349,53 +352,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             __syncwarp();
             const bool q_here = wait(&s_q, seg & 1);
             ok = ok && q_here;
-            auto pv = [&](int x, uint32_t t, bool fresh) {   // P V of tile t
-                const int st = t & 1;
-                ok = ok && wait(&s_pfull[x], n_side[x] & 1) && wait(&s_vfull[st], (t >> 1) & 1);
+            const int steps = 2 * s.tiles;
+            auto qk = [&](int x, int u) {   // S of step u
+                const uint32_t t = tile + u / 2, st = t & 1;
+                ok = ok && wait(&s_kfull[st], (t >> 1) & 1);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t v_lo = sdesc_lo(smem_u32(sV + st * kTile), kHalf);
+                const uint32_t q_lo = sdesc_lo(smem_u32(sQ + x * kTile), 16);
+                const uint32_t k_lo = sdesc_lo(smem_u32(sK + st * kTile + (u & 1) * (kHalf / 2)), 16);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
                     if (elect_one())
-                        umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, sdesc_make(v_lo + kk * 128), idesc_pv,
-                                (!fresh || kk > 0) ? 1u : 0u);
+                        umma_ss(tmem + 128 * x + 64 * (u & 1), sdesc_make(q_lo + off), sdesc_make(k_lo + off), idesc_qk, kk > 0);
+                    __syncwarp();
+                }
+                if (elect_one()) {
+                    umma_commit(&s_sfull[x][u & 1]);
+                    if (x == s.sides - 1 && (u & 1)) umma_commit(&s_kfree[st]);
+                }
+                __syncwarp();
+            };
+            auto pv = [&](int x, int u) {   // O += P V of step u
+                const uint32_t t = tile + u / 2, st = t & 1;
+                ok = ok && wait(&s_pfull[x][u & 1], n_side[x] & 1) && wait(&s_vfull[st], (t >> 1) & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t v_lo = sdesc_lo(smem_u32(sV + st * kTile), kHalf) + (u & 1) * 4 * 128;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (elect_one())
+                        umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 * (u & 1) + kk * 8, sdesc_make(v_lo + kk * 128),
+                                idesc_pv, (u > 0 || kk > 0) ? 1u : 0u);
                     __syncwarp();
                 }
                 if (elect_one()) {
                     umma_commit(&s_pv[x]);
-                    if (x == s.sides - 1) umma_commit(&s_vfree[st]);
+                    if (x == s.sides - 1 && (u & 1)) umma_commit(&s_vfree[st]);
                 }
                 __syncwarp();
-                ++n_side[x];
+                if (u & 1) ++n_side[x];
             };
-            for (int i = 0; ok && i < s.tiles; ++i) {
-                const uint32_t t = tile + i;
-                const int st = t & 1;
-                ok = wait(&s_kfull[st], (t >> 1) & 1);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x >= s.sides) continue;
-                    if (ok && i > 0) pv(x, t - 1, i == 1);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    const uint32_t q_lo = sdesc_lo(smem_u32(sQ + x * kTile), 16), k_lo = sdesc_lo(smem_u32(sK + st * kTile), 16);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        if (elect_one()) umma_ss(tmem + 128 * x, sdesc_make(q_lo + off), sdesc_make(k_lo + off), idesc_qk, kk > 0);
-                        __syncwarp();
-                    }
-                    if (elect_one()) umma_commit(&s_sfull[x]);
-                    __syncwarp();
+            for (int u = 0; u < 2; ++u)
+                for (int x = 0; x < s.sides; ++x) qk(x, u);
+            for (int u = 0; ok && u < steps; ++u)
+                for (int x = 0; x < s.sides; ++x) {
+                    pv(x, u);
+                    if (u + 2 < steps) qk(x, u + 2);
                 }
-                if (ok) {
-                    if (elect_one()) umma_commit(&s_kfree[st]);
-                    __syncwarp();
-                }
-            }
-            for (int x = 0; x < s.sides; ++x)
-                if (ok) pv(x, tile + s.tiles - 1, s.tiles == 1);
                 finish(s);
             }
             if (!ok) {   // the products already issued end before tensor memory is released
@@ -471,75 +475,71 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             if (x < s.sides) {
             const int r = s.row0 + tid;
             const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const uint32_t s_at = tmem + lane_at + 128 * x, o_at = tmem + lane_at + 256 + 128 * x;
+            const uint32_t o_at = tmem + lane_at + 256 + 128 * x;
             const float fac = a.q_scale[((size_t)s.bh * a.tiles128) * 128 + r];
             const int lim = row_limit(a, s.b, r);
             float mref = -INFINITY, l = 0.f;
-            for (int i = 0; ok && i < s.tiles; ++i) {
-                const uint32_t n = n_mine + i;
-                ok = wait(&s_sfull[x], n & 1);
+            for (int u = 0; ok && u < 2 * s.tiles; ++u) {
+                const int j = u & 1;
+                ok = wait(&s_sfull[x][j], (n_mine + u / 2) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const TileInfo& inf = info[(tile + i) % kInfo];
-                const int newest = max(max(inf.newest[0], inf.newest[1]), max(inf.newest[2], inf.newest[3]));
-                // some row of this warp may not see some token of the tile (rows past the last
+                const uint32_t s_at = tmem + lane_at + 128 * x + 64 * j;
+                uint32_t raw_s[2][32];
+                tmem_ld32(s_at, raw_s[0]);
+                tmem_ld32(s_at + 32, raw_s[1]);
+                const TileInfo& inf = info[(tile + u / 2) % kInfo];
+                const int newest = max(inf.newest[2 * j], inf.newest[2 * j + 1]);
+                // some row of this warp may not see some token of the step (rows past the last
                 // are never read back)
                 const bool causal = __any_sync(0xffffffffu, r < a.R && newest > lim);
-                // goes over the products, 32 at a time (the next on their way), with
+                tmem_ld_wait();
+                float v[64];
+#pragma unroll
+                for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(raw_s[e >> 5][e & 31]);
                 // -infinity for what the row does not see
-                auto sweep = [&](auto&& use) {
-                    uint32_t u[2][32];
-                    tmem_ld32(s_at, u[0]);
+                if (causal) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld_wait();
-                        if (c < 3) tmem_ld32(s_at + 32 * (c + 1), u[(c + 1) & 1]);
-                        float v[32];
+                    for (int e = 0; e < 64; e += 4) {
+                        const int4 q = *reinterpret_cast<const int4*>(&inf.pos[64 * j + e]);
+                        v[e] = q.x <= lim ? v[e] : -INFINITY;
+                        v[e + 1] = q.y <= lim ? v[e + 1] : -INFINITY;
+                        v[e + 2] = q.z <= lim ? v[e + 2] : -INFINITY;
+                        v[e + 3] = q.w <= lim ? v[e + 3] : -INFINITY;
+                    }
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[c & 1][e]);
-                        if (causal) {
+                    for (int c = 0; c < 2; ++c)
+                        if (inf.live[2 * j + c] != 0xffffffffu) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const int4 q = *reinterpret_cast<const int4*>(&inf.pos[32 * c + e]);
-                                v[e] = q.x <= lim ? v[e] : -INFINITY;
-                                v[e + 1] = q.y <= lim ? v[e + 1] : -INFINITY;
-                                v[e + 2] = q.z <= lim ? v[e + 2] : -INFINITY;
-                                v[e + 3] = q.w <= lim ? v[e + 3] : -INFINITY;
-                            }
-                        } else if (inf.live[c] != 0xffffffffu) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 q = *reinterpret_cast<const float4*>(&inf.bias[32 * c + e]);
+                            for (int e = 32 * c; e < 32 * c + 32; e += 4) {
+                                const float4 q = *reinterpret_cast<const float4*>(&inf.bias[64 * j + e]);
                                 v[e] += q.x, v[e + 1] += q.y, v[e + 2] += q.z, v[e + 3] += q.w;
                             }
                         }
-                        use(c, v);
-                    }
-                };
-                float top[2] = {-INFINITY, -INFINITY};
-                sweep([&](int, const float (&v)[32]) {
+                }
+                float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        top[0] = fmaxf(top[0], fmaxf(v[e], v[e + 1]));
-                        top[1] = fmaxf(top[1], fmaxf(v[e + 2], v[e + 3]));
-                    }
-                });
-                const float mn = fmaxf(top[0], top[1]) * fac - kShift;
+                for (int e = 4; e < 64; e += 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], e + 4 + k < 64 ? fmaxf(v[e + k], v[e + 4 + k]) : v[e + k]);
+                }
+                const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac - kShift;
                 const bool grow = mn > mref + kLag;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float k = grow ? ex2(mref - mn) : 1.f;   // 0 from the initial -inf
-                    if (i > 0) {
-                        ok = wait(&s_pv[x], (n - 1) & 1);
+                    if (u > 0) {
+                        ok = wait(&s_pv[x], (u - 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_ld32(o_at + 32 * c, v);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            tmem_ld16(o_at + 16 * c, y);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * k);
-                            tmem_st32(o_at + 32 * c, v);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * k);
+                            tmem_st16(o_at + 16 * c, y);
                         }
                         tmem_st_wait();
                     }
@@ -550,24 +550,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 }
                 const float ref = mref == -INFINITY ? 0.f : -mref;   // none seen so far: 2^-inf
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
-                sweep([&](int c, const float (&v)[32]) {
-                    uint32_t p[16];
+                uint32_t p[32];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float y = ex2(fmaf(v[2 * e], fac, ref)), z = ex2(fmaf(v[2 * e + 1], fac, ref));
-                        part[(2 * e) & 3] += y;
-                        part[(2 * e + 1) & 3] += z;
-                        const __half2 h = __floats2half2_rn(y, z);
-                        p[e] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    tmem_st16(s_at + 16 * c, p);   // over products that have been read
-                });
+                for (int e = 0; e < 32; ++e) {
+                    const float y = ex2(fmaf(v[2 * e], fac, ref)), z = ex2(fmaf(v[2 * e + 1], fac, ref));
+                    part[(2 * e) & 3] += y;
+                    part[(2 * e + 1) & 3] += z;
+                    const __half2 h = __floats2half2_rn(y, z);
+                    p[e] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                tmem_st32(s_at, p);   // over products that have been read
                 l += (part[0] + part[1]) + (part[2] + part[3]);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&s_pfull[x]);
+                mbar_arrive(&s_pfull[x][j]);
             }
-            if (ok) ok = wait(&s_pv[x], (n_mine + s.tiles - 1) & 1);
+            if (ok) ok = wait(&s_pv[x], 1);   // an even number of steps: the last is odd
             if (ok) {
                 tc_fence_after();
                 const bool whole = s.blk0 == 0 && s.tiles == s.nblk;
