@@ -210,8 +210,8 @@ __device__ __forceinline__ void part_range(const pbsa_qk_config& c, int which, i
 }
 
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(32 * kWarps) qk_fwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = sizeof(T) == 2 ? 4 : 2;
+__global__ void __launch_bounds__(32 * kWarps, 4) qk_fwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = sizeof(T) == 2 ? 3 : 2;
     const pbsa_qk_config& c = a.c;
     const int lane = threadIdx.x & 31, row = lane / kLanes;
     const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -221,6 +221,17 @@ __global__ void __launch_bounds__(32 * kWarps) qk_fwd_kernel(QkArgs a, int heads
     const int hi = min(lo + heads_per_item, c.Hq + c.Hkv);
     const long long b = token / c.T, t = token % c.T;
     const Rotation<D, IL> rot(c, lane);
+    Raw8<T> raw[kUnroll];
+    auto fetch = [&](int which, int h, int h1) {
+        const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].b + t * a.sx[which].t + 8 * rot.chunk;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) raw[u] = load8(x + min(h + u * kRows + row, h1 - 1) * a.sx[which].h);
+    };
+    // the first heads are on their way while the token's position is looked up
+    const int first = lo >= c.Hq;
+    int f0, f1;
+    part_range(c, first, lo, hi, f0, f1);
+    fetch(first, f0, f1);
     Turn<IL> turn;
     if (!rot.load(a, token, turn)) {
         if (lane == 0) set_status(a.status, PBSA_ERR_DEVICE_CHECK);
@@ -231,17 +242,11 @@ __global__ void __launch_bounds__(32 * kWarps) qk_fwd_kernel(QkArgs a, int heads
         int h0, h1;
         part_range(c, which, lo, hi, h0, h1);
         if (h0 >= h1) continue;
-        const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].b + t * a.sx[which].t + 8 * rot.chunk;
         T* y = static_cast<T*>(a.y[which]) + b * a.sy[which].b + t * a.sy[which].t + 8 * rot.chunk;
         float w[8];
         load_weights(a.w[which], rot.chunk, w);
         for (int h = h0; h < h1; h += kRows * kUnroll) {
-            Raw8<T> raw[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int hh = min(h + u * kRows + row, h1 - 1);
-                raw[u] = load8(x + hh * a.sx[which].h);
-            }
+            if (which != first || h != h0) fetch(which, h, h1);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 if (h + u * kRows >= h1) break;
@@ -262,8 +267,8 @@ __global__ void __launch_bounds__(32 * kWarps) qk_fwd_kernel(QkArgs a, int heads
 }
 
 template <typename T, typename G, int D, bool IL>
-__global__ void __launch_bounds__(32 * kWarps) qk_bwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = sizeof(T) == 2 ? 2 : 1;
+__global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = sizeof(T) == 2 ? 3 : 1;
     const pbsa_qk_config& c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane / kLanes;
     const Rotation<D, IL> rot(c, lane);
@@ -276,6 +281,23 @@ __global__ void __launch_bounds__(32 * kWarps) qk_bwd_kernel(QkArgs a, int heads
         const int lo = (int)(item % items_per_token) * heads_per_item;
         const int hi = min(lo + heads_per_item, c.Hq + c.Hkv);
         const long long b = token / c.T, t = token % c.T;
+        Raw8<T> rx[kUnroll];
+        Raw8<G> rg[kUnroll];
+        auto fetch = [&](int which, int h, int h1) {
+            const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].b + t * a.sx[which].t + 8 * rot.chunk;
+            const G* gy = static_cast<const G*>(a.gy[which]) + b * a.sg[which].b + t * a.sg[which].t + 8 * rot.chunk;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int hh = min(h + u * kRows + row, h1 - 1);
+                rx[u] = load8(x + hh * a.sx[which].h);
+                rg[u] = load8(gy + hh * a.sg[which].h);
+            }
+        };
+        // the first heads are on their way while the token's position is looked up
+        const int first = lo >= c.Hq;
+        int f0, f1;
+        part_range(c, first, lo, hi, f0, f1);
+        fetch(first, f0, f1);
         Turn<IL> turn;
         if (!rot.load(a, token, turn)) {
             if (lane == 0) set_status(a.status, PBSA_ERR_DEVICE_CHECK);
@@ -286,20 +308,11 @@ __global__ void __launch_bounds__(32 * kWarps) qk_bwd_kernel(QkArgs a, int heads
             int h0, h1;
             part_range(c, which, lo, hi, h0, h1);
             if (h0 >= h1) continue;
-            const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].b + t * a.sx[which].t + 8 * rot.chunk;
-            const G* gy = static_cast<const G*>(a.gy[which]) + b * a.sg[which].b + t * a.sg[which].t + 8 * rot.chunk;
             T* dx = static_cast<T*>(a.y[which]) + b * a.sy[which].b + t * a.sy[which].t + 8 * rot.chunk;
             float w[8];
             load_weights(a.w[which], rot.chunk, w);
             for (int h = h0; h < h1; h += kRows * kUnroll) {
-                Raw8<T> rx[kUnroll];
-                Raw8<G> rg[kUnroll];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int hh = min(h + u * kRows + row, h1 - 1);
-                    rx[u] = load8(x + hh * a.sx[which].h);
-                    rg[u] = load8(gy + hh * a.sg[which].h);
-                }
+                if (which != first || h != h0) fetch(which, h, h1);
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
                     if (h + u * kRows >= h1) break;
@@ -417,7 +430,7 @@ int qk_bwd_blocks(const pbsa_qk_config& c) {
     if (tokens == 0) return 0;
     const int per = heads_per_item(c);
     const long long need = (tokens * ((c.Hq + c.Hkv + per - 1) / per) + kWarps - 1) / kWarps;
-    return (int)(need < kSMs * 4 ? need : kSMs * 4);
+    return (int)(need < kSMs * 2 ? need : kSMs * 2);
 }
 
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t st) {

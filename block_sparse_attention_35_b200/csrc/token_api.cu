@@ -113,7 +113,8 @@ int check_cache(const pbsa_kv4_cache* cache) {
 // Tokens of a kv4 call: the grid and index types hold for these.
 int check_tokens(const pbsa_kv4_config* c, int T) {
     if (T < 0) return api_failf(PBSA_ERR_ARG, "T %d < 0", T);
-    if ((long long)T * (c->Hq / c->Hkv) > (1 << 20) || (long long)c->B * T * c->Hq > 0x7fffffffll)
+    if ((long long)T * (c->Hq / c->Hkv) > (1 << 20) || (long long)c->B * T * c->Hq > 0x7fffffffll ||
+        (long long)T * c->Hkv * (c->D / 16) > 0x7fffff00ll)
         return api_failf(PBSA_ERR_UNSUPPORTED, "T %d: too many query rows in one call", T);
     return PBSA_OK;
 }
@@ -260,7 +261,8 @@ int pbsa_kv4_read(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cache, const
     CHECK(validate(cfg));
     if (n < 0) return api_failf(PBSA_ERR_ARG, "n %d < 0", n);
     if (!rows && n > cfg->capacity) return api_failf(PBSA_ERR_ARG, "n %d > capacity %d", n, cfg->capacity);
-    if ((long long)cfg->B * cfg->Hkv * n * (cfg->D / 16) > (1ll << 36))
+    const long long row_blocks = (long long)n * (cfg->D / 16);
+    if (row_blocks > 0x7fffff00ll || (long long)cfg->B * cfg->Hkv * ((row_blocks + 255) / 256) > 0x7fffffffll)
         return api_failf(PBSA_ERR_UNSUPPORTED, "n %d: too many rows in one call", n);
     if (n == 0) return PBSA_OK;
     CHECK(check_cache(cache));
