@@ -239,10 +239,10 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // A CTA (one per SM) goes through its run of the work list in segments of one (sequence, key
 // head, group of 256 rows).  Warps 0-3 and 4-7 are the softmax of the two sides (one row a
 // thread), 8-11 expand the cache (one key a thread, 128 at a time), 12 issues the products, 64
-// keys at a time: QK of step u + 2 goes right behind PV of step u into the same columns, so that
-// a side's softmax finds its next scores ready when it is done with the last ones.  Tensor
-// memory: two S of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its
-// own S and is the A operand of PV.  One thread's products execute in issue order.
+// keys at a time: QK of step u + 2 follows PV of step u into the same columns, so that a side's
+// softmax finds its next scores ready when it is done with the last ones.  Tensor memory: two S
+// of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its own S and is
+// the A operand of PV.  (Products of different shapes may overlap: QK waits until PV is done.)
 constexpr int kChunkThreads = 13 * 32;
 constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
 
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     uint8_t* sV = sK + 2 * kTile;      // [2][kTile]
     TileInfo* info = reinterpret_cast<TileInfo*>(sV + 2 * kTile);   // [kInfo]
     __shared__ __align__(8) uint64_t s_q, s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2];
-    __shared__ __align__(8) uint64_t s_sfull[2][2], s_pfull[2][2], s_pv[2], s_drain;   // by side, S
+    __shared__ __align__(8) uint64_t s_sfull[2][2], s_pfull[2][2], s_pv[2][2], s_drain;   // by side, S
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&s_sfull[i][j], 1);
                 mbar_init(&s_pfull[i][j], 128);
+                mbar_init(&s_pv[i][j], 1);
             }
-            mbar_init(&s_pv[i], 1);
         }
         fence_barrier_init();
     }
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             };
             auto pv = [&](int x, int u) {   // O += P V of step u
                 const uint32_t t = tile + u / 2, st = t & 1;
-                ok = ok && wait(&s_pfull[x][u & 1], n_side[x] & 1) && wait(&s_vfull[st], (t >> 1) & 1);
+                ok = ok && wait(&s_pfull[x][u & 1], (n_side[x] + u / 2) & 1) && wait(&s_vfull[st], (t >> 1) & 1);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t v_lo = sdesc_lo(smem_u32(sV + st * kTile), kHalf) + (u & 1) * 4 * 128;
@@ -387,19 +387,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     __syncwarp();
                 }
                 if (elect_one()) {
-                    umma_commit(&s_pv[x]);
+                    umma_commit(&s_pv[x][u & 1]);
                     if (x == s.sides - 1 && (u & 1)) umma_commit(&s_vfree[st]);
                 }
                 __syncwarp();
-                if (u & 1) ++n_side[x];
             };
             for (int u = 0; u < 2; ++u)
                 for (int x = 0; x < s.sides; ++x) qk(x, u);
-            for (int u = 0; ok && u < steps; ++u)
-                for (int x = 0; x < s.sides; ++x) {
-                    pv(x, u);
-                    if (u + 2 < steps) qk(x, u + 2);
+            // S of step u + 2 takes the columns of P of step u: only once PV has read them
+            auto refill = [&](int x, int u) {
+                if (u < 0 || u + 2 >= steps) return;
+                ok = ok && wait(&s_pv[x][u & 1], (n_side[x] + u / 2) & 1);
+                qk(x, u + 2);
+            };
+            for (int u = 0; ok && u < steps; ++u) {
+                pv(0, u);
+                if (s.sides == 2) {   // each side's wait behind the other side's products
+                    refill(1, u - 1);
+                    pv(1, u);
                 }
+                refill(0, u);
+            }
+            for (int x = 0; x < s.sides; ++x) n_side[x] += s.tiles;
                 finish(s);
             }
             if (!ok) {   // the products already issued end before tensor memory is released
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 if (__any_sync(0xffffffffu, grow)) {
                     const float k = grow ? ex2(mref - mn) : 1.f;   // 0 from the initial -inf
                     if (u > 0) {
-                        ok = wait(&s_pv[x], (u - 1) & 1);
+                        ok = wait(&s_pv[x][(u - 1) & 1], (n_mine + (u - 1) / 2) & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -565,7 +574,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 tc_fence_before();
                 mbar_arrive(&s_pfull[x][j]);
             }
-            if (ok) ok = wait(&s_pv[x], 1);   // an even number of steps: the last is odd
+            if (ok) ok = wait(&s_pv[x][1], (n_mine + s.tiles - 1) & 1);   // an even number of steps
             if (ok) {
                 tc_fence_after();
                 const bool whole = s.blk0 == 0 && s.tiles == s.nblk;

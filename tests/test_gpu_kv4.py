@@ -241,6 +241,47 @@ def test_chunks(cuda_dev, D, dtype, Hq, Hkv, T, N, lens):
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("Hkv,G,T", [(8, 1, 128), (4, 1, 300), (2, 3, 256), (12, 2, 390)])
+def test_chunks_of_many_tiles(cuda_dev, D, dtype, Hkv, G, T):
+    """Many 128-key tiles a CTA, in segments of one side and of two; against torch in fp64 on the
+    GPU, and three runs bit for bit."""
+    N = 4096
+    c = Cache(cuda_dev, B=2, Hq=Hkv * G, Hkv=Hkv, D=D, N=N, dtype=dtype, seed=T + Hkv)
+    c.pos[torch.rand(c.pos.shape, generator=c.g).to(cuda_dev) < 0.02] = -1
+    lens = [N, 3000]
+    q = c.queries(T, 1.5)
+    runs = []
+    for _ in range(3):
+        mass = c.mass.clone()
+        runs.append((*c.attend(q, None, c.i32(lens), mass), mass))
+    assert int(c.status.item()) == 0
+    for r in runs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(r, runs[0]))
+    out, lse, mass = runs[0]
+    k, v = (torch.tensor(t, device=cuda_dev) for t in c.values())
+    e = torch.finfo(dtype).eps / 2
+    for b in range(2):
+        for h in range(Hkv):
+            j = torch.nonzero(c.pos[b, h, :lens[b]] >= 0).flatten()
+            x = q[b, :, h * G:(h + 1) * G].double()                       # [T, G, D]
+            s = x @ k[b, h, j].T / math.sqrt(D)
+            E = 2.0 ** -19 * (x.abs() @ k[b, h, j].abs().T).amax(-1) / math.sqrt(D)
+            wl = torch.logsumexp(s, -1)
+            p = torch.exp(s - wl[..., None])
+            al = lse[b, h * G:(h + 1) * G].T.double()
+            assert ((al - wl).abs() <= E + 2.0 ** -20 * (1 + wl.abs())).all()
+            wo, vabs = p @ v[b, h, j], p @ v[b, h, j].abs()
+            got = out[b, :, h * G:(h + 1) * G].double()
+            tol = e * wo.abs() + (2 * E + 2.0 ** -11 + 2.0 ** -18)[..., None] * vabs
+            tol = tol + N * 2.0 ** -32 * v[b, h, j].abs().max() + 2.0 ** -25
+            assert ((got - wo).abs() <= tol).all()
+            wm = p.sum((0, 1))
+            rel = 2 * E.max() + 2.0 ** -19 * (1 + wl.abs().max())
+            want = c.mass[b, h, j].double() + wm
+            assert ((mass[b, h, j].double() - want).abs() <= rel * wm + T * G * 2.0 ** -24 * wm + 2.0 ** -23 * want).all()
+
+
 def test_chunk_of_a_long_cache(cuda_dev):
     """Parts of one head on many CTAs, an empty sequence and garbage in rows without a token."""
     c = Cache(cuda_dev, B=3, Hq=2, Hkv=1, D=128, N=4096, seed=21)
