@@ -264,6 +264,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                 const uint32_t at_stage = stage * (uint32_t)sizeof(Block<D>);
                 Keys<D> x;
                 load_keys(x, my_kc + at_stage, my_ks + at_stage, my_pos + at_stage / 4, lane);
+                uint32_t v[4][D / 64], vs[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = (i & 1) + 8 * (i >> 1);
+                    load_words(v[i], my_vc + at_stage + j * (D / 2));
+                    vs[i] = my_vs[at_stage + j * (D / 16)];
+                }
                 // s[n][i]: key g + 8 (i >> 1), row 2c + (i & 1) of group n
                 float s[NT][4];
 #pragma unroll
@@ -342,13 +349,6 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                         const __half2 h = __floats2half2_rn(s[n][2 * i], s[n][2 * i + 1]);
                         p[n][i] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
                     }
-                }
-                uint32_t v[4][D / 64], vs[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = (i & 1) + 8 * (i >> 1);
-                    load_words(v[i], my_vc + at_stage + j * (D / 2));
-                    vs[i] = my_vs[at_stage + j * (D / 16)];
                 }
                 const uint32_t vs0 = e4m3x2_to_half2((uint16_t)(__byte_perm(vs[0], vs[1], 0x0040) & vmask[0]));
                 const uint32_t vs1 = e4m3x2_to_half2((uint16_t)(__byte_perm(vs[2], vs[3], 0x0040) & vmask[1]));

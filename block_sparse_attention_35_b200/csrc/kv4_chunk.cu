@@ -238,12 +238,12 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // --------------------------------------------------------------------------- attention
 // A CTA (one per SM) goes through its run of the work list in segments of one (sequence, key
 // head, group of 256 rows).  Warps 0-3 and 4-7 are the softmax of the two sides (one row a
-// thread), 8-11 expand the cache (one key a thread, 128 at a time), 12 issues the products, 64
-// keys at a time: QK of step u + 2 follows PV of step u into the same columns, so that a side's
+// thread), 8-11 expand the cache (one key a thread, 128 at a time), 12 and 13 issue the products
+// of a side each, 64 keys at a time: QK of step u + 2 follows PV of step u into the same columns, so that a side's
 // softmax finds its next scores ready when it is done with the last ones.  Tensor memory: two S
 // of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its own S and is
 // the A operand of PV.  (Products of different shapes may overlap: QK waits until PV is done.)
-constexpr int kChunkThreads = 13 * 32;
+constexpr int kChunkThreads = 14 * 32;
 constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
 
 struct TileInfo {
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     uint8_t* sK = sQ + 2 * kTile;      // [2][kTile]
     uint8_t* sV = sK + 2 * kTile;      // [2][kTile]
     TileInfo* info = reinterpret_cast<TileInfo*>(sV + 2 * kTile);   // [kInfo]
-    __shared__ __align__(8) uint64_t s_q, s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2];
-    __shared__ __align__(8) uint64_t s_sfull[2][2], s_pfull[2][2], s_pv[2][2], s_drain;   // by side, S
+    __shared__ __align__(8) uint64_t s_q[2], s_kfull[2], s_kfree[2], s_vfull[2], s_vfree[2];
+    __shared__ __align__(8) uint64_t s_sfull[2][2], s_pfull[2][2], s_pv[2][2], s_drain[2];   // by side, S
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -276,13 +276,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     }
     if (tid == 0) {
         s_abort = 0;
-        mbar_init(&s_q, 1);
-        mbar_init(&s_drain, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_kfull[i], 128);
             mbar_init(&s_vfull[i], 128);
-            mbar_init(&s_kfree[i], 1);
-            mbar_init(&s_vfree[i], 1);
+            mbar_init(&s_kfree[i], 2);   // an arrival for each side
+            mbar_init(&s_vfree[i], 2);
+            mbar_init(&s_q[i], 1);
+            mbar_init(&s_drain[i], 1);
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&s_sfull[i][j], 1);
                 mbar_init(&s_pfull[i][j], 128);
@@ -337,87 +337,84 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     };
 
     if (warp >= 8) {
-        if (warp == 12) {
+        if (warp >= 12) {
             // ------------------------------------------------- queries, and the products
-            uint32_t n_side[2] = {0, 0};   // tiles so far of a side (the second rests in a group of at most 128 rows)
-            for (int seg = 0; left > 0; ++seg) {
-                const Segment s = segment();
+            const int x = warp - 12;
             constexpr uint32_t idesc_qk = idesc_f16(128, 64, false), idesc_pv = idesc_f16(128, D, true);
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&s_q, s.sides * kTile);
-                for (int x = 0; x < s.sides; ++x)
-                    bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)s.bh * a.tiles128 + s.row0 / 128 + x) * kTile,
-                              kTile, smem_u32(&s_q));
-            }
-            __syncwarp();
-            const bool q_here = wait(&s_q, seg & 1);
-            ok = ok && q_here;
-            const int steps = 2 * s.tiles;
-            auto qk = [&](int x, int u) {   // S of step u
-                const uint32_t t = tile + u / 2, st = t & 1;
-                ok = ok && wait(&s_kfull[st], (t >> 1) & 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t q_lo = sdesc_lo(smem_u32(sQ + x * kTile), 16);
-                const uint32_t k_lo = sdesc_lo(smem_u32(sK + st * kTile + (u & 1) * (kHalf / 2)), 16);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                    if (elect_one())
-                        umma_ss(tmem + 128 * x + 64 * (u & 1), sdesc_make(q_lo + off), sdesc_make(k_lo + off), idesc_qk, kk > 0);
+            uint32_t n_mine = 0;   // tiles so far of this side (the second rests in a group of at most 128 rows)
+            int n_seg = 0;
+            while (left > 0) {
+                const Segment s = segment();
+                if (x < s.sides) {
+                    const int steps = 2 * s.tiles, ends = 3 - s.sides;   // arrivals that free a tile
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&s_q[x], kTile);
+                        bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)s.bh * a.tiles128 + s.row0 / 128 + x) * kTile,
+                                  kTile, smem_u32(&s_q[x]));
+                    }
                     __syncwarp();
-                }
-                if (elect_one()) {
-                    umma_commit(&s_sfull[x][u & 1]);
-                    if (x == s.sides - 1 && (u & 1)) umma_commit(&s_kfree[st]);
-                }
-                __syncwarp();
-            };
-            auto pv = [&](int x, int u) {   // O += P V of step u
-                const uint32_t t = tile + u / 2, st = t & 1;
-                ok = ok && wait(&s_pfull[x][u & 1], (n_side[x] + u / 2) & 1) && wait(&s_vfull[st], (t >> 1) & 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t v_lo = sdesc_lo(smem_u32(sV + st * kTile), kHalf) + (u & 1) * 4 * 128;
+                    const bool q_here = wait(&s_q[x], n_seg & 1);
+                    ok = ok && q_here;
+                    const uint32_t q_lo = sdesc_lo(smem_u32(sQ + x * kTile), 16);
+                    auto qk = [&](int u) {   // S of step u
+                        const uint32_t t = tile + u / 2, st = t & 1;
+                        ok = ok && wait(&s_kfull[st], (t >> 1) & 1);
+                        if (!ok) return;
+                        tc_fence_after();
+                        const uint32_t k_lo = sdesc_lo(smem_u32(sK + st * kTile + (u & 1) * (kHalf / 2)), 16);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (elect_one())
-                        umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 * (u & 1) + kk * 8, sdesc_make(v_lo + kk * 128),
-                                idesc_pv, (u > 0 || kk > 0) ? 1u : 0u);
-                    __syncwarp();
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                            if (elect_one())
+                                umma_ss(tmem + 128 * x + 64 * (u & 1), sdesc_make(q_lo + off), sdesc_make(k_lo + off), idesc_qk, kk > 0);
+                            __syncwarp();
+                        }
+                        if (elect_one()) {
+                            umma_commit(&s_sfull[x][u & 1]);
+                            if (u & 1)
+                                for (int i = 0; i < ends; ++i) umma_commit(&s_kfree[st]);
+                        }
+                        __syncwarp();
+                    };
+                    qk(0);
+                    qk(1);
+                    for (int u = 0; ok && u < steps; ++u) {
+                        // O += P V of step u
+                        const uint32_t t = tile + u / 2, st = t & 1, parity = (n_mine + u / 2) & 1;
+                        ok = wait(&s_pfull[x][u & 1], parity) && wait(&s_vfull[st], (t >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t v_lo = sdesc_lo(smem_u32(sV + st * kTile), kHalf) + (u & 1) * 4 * 128;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (elect_one())
+                                umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 * (u & 1) + kk * 8, sdesc_make(v_lo + kk * 128),
+                                        idesc_pv, (u > 0 || kk > 0) ? 1u : 0u);
+                            __syncwarp();
+                        }
+                        if (elect_one()) {
+                            umma_commit(&s_pv[x][u & 1]);
+                            if (u & 1)
+                                for (int i = 0; i < ends; ++i) umma_commit(&s_vfree[st]);
+                        }
+                        __syncwarp();
+                        // S of step u + 2 takes the columns of P of step u: only once PV has read them
+                        if (u + 2 < steps) {
+                            ok = wait(&s_pv[x][u & 1], parity);
+                            qk(u + 2);
+                        }
+                    }
+                    n_mine += s.tiles;
+                    ++n_seg;
                 }
-                if (elect_one()) {
-                    umma_commit(&s_pv[x][u & 1]);
-                    if (x == s.sides - 1 && (u & 1)) umma_commit(&s_vfree[st]);
-                }
-                __syncwarp();
-            };
-            for (int u = 0; u < 2; ++u)
-                for (int x = 0; x < s.sides; ++x) qk(x, u);
-            // S of step u + 2 takes the columns of P of step u: only once PV has read them
-            auto refill = [&](int x, int u) {
-                if (u < 0 || u + 2 >= steps) return;
-                ok = ok && wait(&s_pv[x][u & 1], (n_side[x] + u / 2) & 1);
-                qk(x, u + 2);
-            };
-            for (int u = 0; ok && u < steps; ++u) {
-                pv(0, u);
-                if (s.sides == 2) {   // each side's wait behind the other side's products
-                    refill(1, u - 1);
-                    pv(1, u);
-                }
-                refill(0, u);
-            }
-            for (int x = 0; x < s.sides; ++x) n_side[x] += s.tiles;
                 finish(s);
             }
             if (!ok) {   // the products already issued end before tensor memory is released
-                if (elect_one()) umma_commit(&s_drain);
+                if (elect_one()) umma_commit(&s_drain[x]);
                 __syncwarp();
-                mbar_wait_drain(&s_drain, 0, 100000000ull);
+                mbar_wait_drain(&s_drain[x], 0, 100000000ull);
             }
-            tmem_dealloc(tmem, 512);
-        } else if (warp < 12) {
+        } else {
             // -------------------------------------------------- the cache, into operands
             while (left > 0) {
                 const Segment s = segment();
@@ -609,6 +606,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             }
             finish(s);
         }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
