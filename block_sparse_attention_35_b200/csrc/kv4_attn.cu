@@ -107,7 +107,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const Keys<D>& x, QF q
 }
 
 // A CTA takes a run of the work list and goes through it segment by segment, a segment being
-// the blocks of one (sequence, key head, group of 8 NT rows).  One warp asks for block after
+// the blocks of one (sequence, key head); all of its rows, at most 8 NT.  One warp asks for block after
 // block, across segment borders, into a ring in shared memory (bulk copies).  The others take
 // sixteen of a block's keys each; each has its own running maximum, sum and output, which are
 // joined in shared memory at the end of a segment.  A segment that covers its head's keys goes
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
             const uint32_t rows = min(kBlock, N - row);
             Block<D>& s = ring[stage];
             const uint32_t bar = smem_u32(&s_full[stage]);
-            const size_t first = ((size_t)at.b * a.k.c.Hkv + at.h / a.groups) * N + row;
+            const size_t first = ((size_t)at.b * a.k.c.Hkv + at.h) * N + row;
             const pbsa_kv4_cache& k = a.k.cache;
             mbar_arrive_expect_tx(&s_full[stage], rows * (D + D / 8 + 4));
             bulk_load(smem_u32(s.kc), k.k_codes + first * (D / 2), rows * (D / 2), bar);
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
     const uint8_t* my_vc = ring->vc[warp * kUnit + 2 * c] + g * (D / 16);
     const uint8_t* my_vs = ring->vs[warp * kUnit + 2 * c] + g * (D / 16) / 8;
     for (bool first = true; n_use < total; first = false) {
-        const int b = at.b, hkv = at.h / a.groups, grp = at.h - hkv * a.groups, len = at.len, blk0 = at.blk;
-        const int bh = b * a.k.c.Hkv + hkv, row0 = grp * kRows;
+        const int b = at.b, hkv = at.h, len = at.len, blk0 = at.blk;
+        const int bh = b * a.k.c.Hkv + hkv;
         const int nblk = blocks_of(a, len), blk1 = min(nblk, blk0 + total - n_use);
         // queries into operand order, D / 4 lanes to a row: lane 4 g + c of step j and row group
         // n holds row 8 n + g's channels c D / 4 + 4 j .. + 3
@@ -205,17 +205,16 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
         for (int r0 = 0; r0 < kRows; r0 += kThreads / (D / 4)) {
             const int r = r0 + (int)threadIdx.x / (D / 4), ch4 = threadIdx.x % (D / 4);
             float f;
-            const uint2 v = scale_query4<D>(a, load_query4<T>(a, b, hkv, row0 + r, 4 * ch4), f);
+            const uint2 v = scale_query4<D>(a, load_query4<T>(a, b, hkv, r, 4 * ch4), f);
             const int j = ch4 % kSteps, slot = (r & 7) * 4 + ch4 / kSteps;
             if (r < kRows) {
                 q_sm[(j * NT + r / 8) * 32 + slot] = v;
                 if (ch4 == 0) {
                     fac_sm[r] = f;
-                    lim_sm[r] = row_limit(a, b, row0 + r);
+                    lim_sm[r] = row_limit(a, b, r);
                 }
-                const int tile = row0 / 8 + r / 8;
-                if (a.q_frag && blk0 == 0 && tile < a.tiles8) {
-                    const size_t to = (size_t)bh * a.tiles8 + tile;
+                if (a.q_frag && blk0 == 0 && r / 8 < a.tiles8) {
+                    const size_t to = (size_t)bh * a.tiles8 + r / 8;
                     a.q_frag[(to * kSteps + j) * 32 + slot] = v;
                     if (ch4 == 0) a.q_fac[to * 8 + (r & 7)] = f;
                 }
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
         auto fac = [&](int n, int i) -> float { return NT == 1 ? fac1[i] : fac_sm[8 * n + 2 * c + i]; };
         auto lim = [&](int n, int i) -> int { return NT == 1 ? lim1[i] : lim_sm[8 * n + 2 * c + i]; };
         auto qf = [&](int j, int n) -> uint2 { return NT == 1 ? qr[NT == 1 ? j : 0] : q_sm[(j * NT + n) * 32 + lane]; };
-        const bool choosy = a.k.q_pos || row0 + kRows > a.R;   // some row may not see some key
+        const bool choosy = a.k.q_pos || kRows > a.R;   // some row may not see some key
         float* lg = kLogits ? a.logits + ((size_t)bh * a.R + 2 * c) * N + g : nullptr;
 
         float mref[NT][2], thr[NT][2], l[NT][2], o[NT][kSteps][4];
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
         const size_t slot = ((size_t)blockIdx.x * 2 + (blk0 == 0)) * kRows;
         for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-            if (row0 + r >= a.R) break;
+            if (r >= a.R) break;
             float mx = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, m_sm[k * kRows + r]);
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                 sum += f * l_sm[k * kRows + r];
             }
             if (whole) {
-                finish_row<D, T>(a, b, hkv, row0 + r, d, t, mx, sum);
+                finish_row<D, T>(a, b, hkv, r, d, t, mx, sum);
             } else {
                 *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = t;
                 if (d == 0) a.part_ml[slot + r] = make_float2(mx, sum);
@@ -596,9 +595,9 @@ int row_groups(int R) { return R <= 8 ? 1 : (R <= 16 ? 2 : 4); }
 bool keeps_logits(int R) { return R <= 8; }
 
 // The split of a call: rows of a group, groups, and CTAs - they fill every SM once, and none
-// has less than a block.
-void plan(const pbsa_kv4_config& c, int R, AttnArgs& a) {
-    const bool chunk = chunk_takes(c, R);
+// has less than a block.  Returns the blocks of a full cache.
+long long plan(const pbsa_kv4_config& c, int R, AttnArgs& a) {
+    const bool chunk = chunk_takes(R);
     const int nt = row_groups(R), per_sm = !chunk && nt == 1 ? 2 : 1;
     a.rows = chunk ? kChunkRows : 8 * nt;
     a.groups = (R + a.rows - 1) / a.rows;
@@ -608,6 +607,7 @@ void plan(const pbsa_kv4_config& c, int R, AttnArgs& a) {
     a.tiles128 = (R + 127) / 128;
     const long long blocks = (long long)c.B * a.heads * ((c.capacity + a.block - 1) / a.block);
     a.ctas = (int)(blocks < kSMs * per_sm ? blocks : kSMs * per_sm);
+    return blocks;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -629,7 +629,7 @@ struct Layout {
         part_o = take(slots * c.D * sizeof(float));
         part_ml = take(slots * sizeof(float2));
         logits = q_frag = q_fac = q_tile = q_scale = at;
-        if (chunk_takes(c, R)) {
+        if (chunk_takes(R)) {
             q_tile = take(bh * a.tiles128 * 128 * c.D * 2);
             q_scale = take(bh * a.tiles128 * 128 * sizeof(float));
         } else if (keeps_logits(R)) {
@@ -654,7 +654,7 @@ cudaError_t run_rows(const AttnArgs& a, cudaStream_t st) {
 
 template <int D, typename T>
 cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
-    const bool chunk = chunk_takes(a.k.c, a.R);
+    const bool chunk = chunk_takes(a.R);
     cudaError_t e;
     if (chunk) e = launch_chunk_attn(a, st);
     else if (a.rows == 8) e = a.k.mass ? run_rows<D, 1, T, true>(a, st) : run_rows<D, 1, T, false>(a, st);
@@ -684,6 +684,11 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+bool kv4_attn_fits(const pbsa_kv4_config& c, int T) {
+    AttnArgs a{};
+    return plan(c, T * (c.Hq / c.Hkv), a) < (1ll << 31);
+}
+
 size_t kv4_attn_workspace(const pbsa_kv4_config& c, int T) { return Layout(c, T * (c.Hq / c.Hkv)).bytes; }
 
 cudaError_t launch_kv4_attn(const Kv4Args& k, cudaStream_t st) {
@@ -696,7 +701,7 @@ cudaError_t launch_kv4_attn(const Kv4Args& k, cudaStream_t st) {
     char* w = static_cast<char*>(k.workspace);
     a.part_o = reinterpret_cast<float*>(w + lay.part_o);
     a.part_ml = reinterpret_cast<float2*>(w + lay.part_ml);
-    if (chunk_takes(k.c, a.R)) {
+    if (chunk_takes(a.R)) {
         a.q_tile = reinterpret_cast<uint8_t*>(w + lay.q_tile);
         a.q_scale = reinterpret_cast<float*>(w + lay.q_scale);
     } else if (k.mass && keeps_logits(a.R)) {

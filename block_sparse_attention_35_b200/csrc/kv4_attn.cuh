@@ -224,8 +224,8 @@ inline cudaError_t launch_after(void (*kernel)(AttnArgs), dim3 grid, int threads
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Many rows (kv4_chunk.cu): bytes of its part of the workspace, and its launches.
-bool chunk_takes(const pbsa_kv4_config& c, int R);
+// Many rows (kv4_chunk.cu): whether it takes a call, and its launches.
+bool chunk_takes(int R);
 cudaError_t launch_chunk_attn(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_mass(const AttnArgs& a, cudaStream_t st);
 constexpr int kChunkRows = 256, kChunkKeys = 128;

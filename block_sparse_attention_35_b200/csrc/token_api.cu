@@ -119,6 +119,13 @@ int check_tokens(const pbsa_kv4_config* c, int T) {
     return PBSA_OK;
 }
 
+int check_queries(const pbsa_kv4_config* c, int T) {
+    CHECK(check_tokens(c, T));
+    if (T > 0 && !pbsa::kv4_attn_fits(*c, T))
+        return api_failf(PBSA_ERR_UNSUPPORTED, "T %d over this cache: too many query rows in one call", T);
+    return PBSA_OK;
+}
+
 pbsa::Kv4Args kv4_args(const pbsa_kv4_config* c, const pbsa_kv4_cache* cache) {
     pbsa::Kv4Args a{};
     a.c = *c;
@@ -225,7 +232,7 @@ int pbsa_qk_norm_rope_bwd(const pbsa_qk_config* cfg, const void* q, const void* 
 int pbsa_validate_kv4_config(const pbsa_kv4_config* cfg) { return validate(cfg); }
 
 size_t pbsa_kv4_workspace_size(const pbsa_kv4_config* cfg, int T) {
-    if (validate(cfg) != PBSA_OK || check_tokens(cfg, T) != PBSA_OK) return 0;
+    if (validate(cfg) != PBSA_OK || check_queries(cfg, T) != PBSA_OK) return 0;
     return T == 0 ? 0 : pbsa::kv4_attn_workspace(*cfg, T);
 }
 
@@ -284,7 +291,7 @@ int pbsa_kv4_attn(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cache, const
                   int T, const int32_t* q_pos, const int32_t* kv_len, void* out, float* lse, float* mass,
                   void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
     CHECK(validate(cfg));
-    CHECK(check_tokens(cfg, T));
+    CHECK(check_queries(cfg, T));
     if (T == 0) return PBSA_OK;
     CHECK(check_cache(cache));
     NEED(q);

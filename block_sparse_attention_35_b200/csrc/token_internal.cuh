@@ -64,6 +64,8 @@ cudaError_t launch_kv4_append(const Kv4Args& a, cudaStream_t st);
 cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t st);
 cudaError_t launch_kv4_attn(const Kv4Args& a, cudaStream_t st);
 size_t kv4_attn_workspace(const pbsa_kv4_config& c, int T);
+// Whether the pieces of work of a call can be counted (below 2^31).
+bool kv4_attn_fits(const pbsa_kv4_config& c, int T);
 
 struct EvictArgs {
     int BH, Hkv, N, n, n_sink;

@@ -428,6 +428,10 @@ def _qk_check(cfg, tensors, q_weight, k_weight, cos, sin, pos, status):
         if cfg.Hkv:
             _want(tk, "k" + name if name[:1] == "_" or not name else name + "k",
                   (cfg.B, cfg.T, cfg.Hkv, cfg.D), dt, dev, True)
+    for name, tq, tk, _ in tensors[-1:]:   # the outputs: every element its own
+        for t in (tq, tk):
+            if t is not None and any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+                _bad("an output has elements that share memory")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             _want(w, name, (cfg.D,), torch.float32, dev)

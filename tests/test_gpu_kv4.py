@@ -198,7 +198,7 @@ def test_append_padding_views_bad_rows_and_non_finite(cuda_dev):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("Hq,Hkv,T", [(1, 1, 1), (4, 2, 1), (8, 1, 1), (12, 1, 1), (6, 2, 3), (5, 5, 7), (9, 1, 2),
-                                      (32, 1, 1), (7, 1, 5), (2, 1, 40)])
+                                      (32, 1, 1), (7, 1, 5), (3, 1, 11), (4, 1, 8), (2, 1, 40)])
 def test_rows_of_every_count(cuda_dev, D, dtype, Hq, Hkv, T):
     """1 to 80 query rows to a key head: all variants, full groups of rows and ragged ones."""
     N = 192

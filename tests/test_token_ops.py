@@ -191,6 +191,9 @@ def test_bad_pointers_and_sizes_are_refused_before_any_launch():
     args = list(attn)
     args[2] = 1 << 20
     refused(lib.pbsa_kv4_attn(ref(kc), ref(ok), *args, None), "too many", P.PBSA_ERR_UNSUPPORTED)
+    # a call whose pieces of work cannot be counted in 31 bits
+    big = P.make_kv4_config(1024, 64, 1, 128, 131072)
+    assert P.library().pbsa_kv4_workspace_size(ref(big), 16384) == 0 and "too many" in P.pbsa_last_error()
     for n, sink, word in ((-1, 0, "n -1"), (65, 0, "n 65"), (1, -1, "n_sink")):
         refused(lib.pbsa_kv4_evict(ref(kc), 256, 256, n, sink, None, 256, 256, None), word)
     for i, name in ((0, "pos"), (1, "mass"), (5, "rows"), (6, "status")):
@@ -246,5 +249,7 @@ def test_binding_refuses_tensors_that_do_not_fit():
         args[i] = bad
         with pytest.raises(P.PBSAError, match=name):
             P.pbsa_qk_norm_rope(qc, *args, st)
+    with pytest.raises(P.PBSAError, match="share memory"):
+        P.pbsa_qk_norm_rope(qc, *good[:7], k[:, :1].expand(2, 3, 2, 64), k, st)
     with pytest.raises(P.PBSAError):
         P.make_qk_config(2, 3, 2, 2, 64, axis_pairs=(8, 8, 8, 8))
