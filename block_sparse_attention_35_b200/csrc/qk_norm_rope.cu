@@ -30,6 +30,7 @@ namespace pbsa {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kFwdCtas = 4, kBwdCtas = 2;   // blocks an SM, by registers
 
 // Eight consecutive channels of a lane, as loaded.
 template <typename T>
@@ -210,7 +211,7 @@ __device__ __forceinline__ void part_range(const pbsa_qk_config& c, int which, i
 }
 
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(32 * kWarps, 4) qk_fwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
+__global__ void __launch_bounds__(32 * kWarps, kFwdCtas) qk_fwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = sizeof(T) == 2 ? 3 : 2;
     const pbsa_qk_config& c = a.c;
     const int lane = threadIdx.x & 31, row = lane / kLanes;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_fwd_kernel(QkArgs a, int he
 }
 
 template <typename T, typename G, int D, bool IL>
-__global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
+__global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qk_bwd_kernel(QkArgs a, int heads_per_item, int items_per_token) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = sizeof(T) == 2 ? 3 : 1;
     const pbsa_qk_config& c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane / kLanes;
@@ -376,22 +377,19 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* partial, int b
 }
 
 // Heads of one work item: all of a token's heads when the tokens alone fill the GPU (the
-// rotation is then loaded once per token), else fewer, down to the heads of one step.
-int heads_per_item(const pbsa_qk_config& c) {
+// rotation is then loaded once per token), else as few as still give every resident warp
+// (`ctas` blocks an SM) an item of its own, down to the heads of one step.
+int heads_per_item(const pbsa_qk_config& c, int ctas) {
     const int heads = c.Hq + c.Hkv, step = 32 / (c.D / 8);
-    const long long tokens = (long long)c.B * c.T, want = (long long)kSMs * kWarps * 4;
-    long long per = heads;
-    if (tokens < want) {
-        const long long items = (want + tokens - 1) / tokens;
-        per = (heads + items - 1) / items;
-    }
-    per = (per + step - 1) / step * step;
-    return (int)(per < step ? step : per);
+    const long long tokens = (long long)c.B * c.T, warps = (long long)kSMs * kWarps * ctas;
+    const long long items = tokens < warps ? warps / tokens : 1;
+    const long long per = (heads + items - 1) / items;
+    return (int)((per + step - 1) / step * step);
 }
 
 template <typename T, int D, bool IL>
 cudaError_t run_fwd(const QkArgs& a, cudaStream_t st) {
-    const int per = heads_per_item(a.c), ipt = (a.c.Hq + a.c.Hkv + per - 1) / per;
+    const int per = heads_per_item(a.c, kFwdCtas), ipt = (a.c.Hq + a.c.Hkv + per - 1) / per;
     const long long items = (long long)a.c.B * a.c.T * ipt;
     qk_fwd_kernel<T, D, IL><<<(unsigned)((items + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a, per, ipt);
     return cudaGetLastError();
@@ -399,7 +397,7 @@ cudaError_t run_fwd(const QkArgs& a, cudaStream_t st) {
 
 template <typename T, typename G, int D, bool IL>
 cudaError_t run_bwd(const QkArgs& a, cudaStream_t st) {
-    const int per = heads_per_item(a.c), ipt = (a.c.Hq + a.c.Hkv + per - 1) / per;
+    const int per = heads_per_item(a.c, kBwdCtas), ipt = (a.c.Hq + a.c.Hkv + per - 1) / per;
     const int blocks = qk_bwd_blocks(a.c);
     if (blocks > 0) {
         qk_bwd_kernel<T, G, D, IL><<<blocks, 32 * kWarps, 0, st>>>(a, per, ipt);
@@ -428,9 +426,9 @@ cudaError_t bwd_shape(const QkArgs& a, cudaStream_t st) {
 int qk_bwd_blocks(const pbsa_qk_config& c) {
     const long long tokens = (long long)c.B * c.T;
     if (tokens == 0) return 0;
-    const int per = heads_per_item(c);
+    const int per = heads_per_item(c, kBwdCtas);
     const long long need = (tokens * ((c.Hq + c.Hkv + per - 1) / per) + kWarps - 1) / kWarps;
-    return (int)(need < kSMs * 2 ? need : kSMs * 2);
+    return (int)(need < kSMs * kBwdCtas ? need : kSMs * kBwdCtas);
 }
 
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t st) {
