@@ -25,6 +25,28 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Two floats in a 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // 32 channels (16 bytes of codes, two scales) of row `row` as four 16-byte chunks of a tile;
 // quarter q of 32 channels each.
 __device__ __forceinline__ void expand32(uint8_t* tile, int row, int q, const uint4& codes, uint32_t scales) {
@@ -73,7 +95,8 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
     uint8_t* sK = sm;
     uint8_t* sQ = sm + kTile;   // [2][kTile]
     __shared__ __align__(8) uint64_t s_qfull[2], s_qfree[2], s_full[2], s_free[2], s_drain;
-    __shared__ __align__(16) float2 s_col[2][2][128];   // factor and -lse of a row; by group of warps, tile
+    // by group of warps and tile: factors of two rows, their -lse; and limits
+    __shared__ __align__(16) float s_col[2][2][64][4];
     __shared__ int s_lim[2][2][128];
     __shared__ float s_sum[128];
     __shared__ uint32_t s_tmem;
@@ -187,14 +210,15 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
         float4 next = column(group);
         for (int t = group; t < tiles; t += 2) {
             const int buf = (t >> 1) & 1;
-            s_col[group][buf][key] = make_float2(next.x, next.y);
+            s_col[group][buf][key >> 1][key & 1] = next.x;
+            s_col[group][buf][key >> 1][2 + (key & 1)] = next.y;
             s_lim[group][buf][key] = __float_as_int(next.z);
             named_bar_sync(1 + group, 128);   // and the columns two tiles back have been read
             next = column(t + 2);
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status));
             if (ok) {
                 tc_fence_after();
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                uint64_t part[2] = {0, 0};
                 uint32_t u[2][16];
                 tmem_ld16(addr, u[0]);
 #pragma unroll
@@ -208,19 +232,20 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
                     }
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float4 col = *reinterpret_cast<const float4*>(&s_col[group][buf][16 * c + e]);
-                        float x = ex2(fmaf(__uint_as_float(u[c & 1][e]), col.x, col.y));
-                        float y = ex2(fmaf(__uint_as_float(u[c & 1][e + 1]), col.z, col.w));
+                        const float4 col = *reinterpret_cast<const float4*>(s_col[group][buf][8 * c + e / 2]);
+                        float2 x = split(fma2(pair(__uint_as_float(u[c & 1][e]), __uint_as_float(u[c & 1][e + 1])),
+                                              pair(col.x, col.y), pair(col.z, col.w)));
+                        x.x = ex2(x.x), x.y = ex2(x.y);
                         if (a.k.q_pos) {
                             const int2 lim = *reinterpret_cast<const int2*>(&s_lim[group][buf][16 * c + e]);
-                            x = pos <= lim.x ? x : 0.f;
-                            y = pos <= lim.y ? y : 0.f;
+                            x.x = pos <= lim.x ? x.x : 0.f;
+                            x.y = pos <= lim.y ? x.y : 0.f;
                         }
-                        part[e & 3] += x;
-                        part[(e + 1) & 3] += y;
+                        part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pair(x.x, x.y));
                     }
                 }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                const float2 sums = split(add2(part[0], part[1]));
+                sum += sums.x + sums.y;
             }
         }
         if (group == 1) s_sum[key] = sum;
@@ -520,7 +545,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
 #pragma unroll
                             for (int e = 32 * c; e < 32 * c + 32; e += 4) {
                                 const float4 q = *reinterpret_cast<const float4*>(&inf.bias[64 * j + e]);
-                                v[e] += q.x, v[e + 1] += q.y, v[e + 2] += q.z, v[e + 3] += q.w;
+                                const float2 y = split(add2(pair(v[e], v[e + 1]), pair(q.x, q.y)));
+                                const float2 z = split(add2(pair(v[e + 2], v[e + 3]), pair(q.z, q.w)));
+                                v[e] = y.x, v[e + 1] = y.y, v[e + 2] = z.x, v[e + 3] = z.y;
                             }
                         }
                 }
@@ -555,18 +582,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     }
                 }
                 const float ref = mref == -INFINITY ? 0.f : -mref;   // none seen so far: 2^-inf
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t fac2 = pair(fac, fac), ref2 = pair(ref, ref);
+                uint64_t part[2] = {0, 0};
                 uint32_t p[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const float y = ex2(fmaf(v[2 * e], fac, ref)), z = ex2(fmaf(v[2 * e + 1], fac, ref));
-                    part[(2 * e) & 3] += y;
-                    part[(2 * e + 1) & 3] += z;
-                    const __half2 h = __floats2half2_rn(y, z);
+                    float2 y = split(fma2(pair(v[2 * e], v[2 * e + 1]), fac2, ref2));
+                    y.x = ex2(y.x), y.y = ex2(y.y);
+                    part[e & 1] = add2(part[e & 1], pair(y.x, y.y));
+                    const __half2 h = __floats2half2_rn(y.x, y.y);
                     p[e] = *reinterpret_cast<const uint32_t*>(&h);
                 }
                 tmem_st32(s_at, p);   // over products that have been read
-                l += (part[0] + part[1]) + (part[2] + part[3]);
+                const float2 sums = split(add2(part[0], part[1]));
+                l += sums.x + sums.y;
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&s_pfull[x][j]);
