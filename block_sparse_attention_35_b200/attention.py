@@ -168,9 +168,10 @@ class SparseForcingAttention:
         return self._heads[key]
 
     def _head_positions(self, pos, first_frame: int):
-        if first_frame == 0:
-            return pos
-        return pos + torch.tensor([first_frame, 0, 0], dtype=torch.int32).to(self.device)
+        if first_frame:
+            pos = pos.clone()
+            pos[..., 0] += first_frame
+        return pos
 
     def norm_rope(self, q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, first_frame: int):
         """RMS-normalises every head of the projected queries and keys [B, frames*T_f, H, D]

@@ -14,7 +14,9 @@
 //
 // append_kernel and read_kernel are bound by HBM: one thread owns one block of sixteen
 // channels, 32 bytes of a 16-bit type against 8 bytes of codes and one scale byte; neighbouring
-// threads own neighbouring blocks, so a warp touches whole sectors on both sides.
+// threads own neighbouring blocks, so a warp touches whole sectors on both sides.  4680 tokens
+// of 12 heads of 128 channels, L2 cold: append 13.7 us (28.8 MB read, 8.1 MB written, to
+// scattered rows), read 10.1 us; one token of 32 x 8 caches 2.9 and 2.6 us, launch and latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

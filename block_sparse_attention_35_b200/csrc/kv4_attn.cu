@@ -116,6 +116,18 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const Keys<D>& x, QF q
 // Keys and values are the row operand of the tensor-core steps (S^T = K Q^T, O^T = V^T P^T),
 // so that rows come in groups of eight and a code is turned into fp16 once, in the register
 // that it is multiplied from.
+//
+// What bounds it (D = 128, L2 cold).  A step of sixteen keys is 2.4 KB and 331 instructions of a
+// warp, 161 of them on the ALU pipe that takes one every other cycle (64 conversions of code
+// pairs): with fourteen computing warps an SM, long caches stream at 4.9 TB/s, three quarters of
+// the copy rate.  Without any arithmetic the same ring streams at 7.4 TB/s, so the ring does not
+// bound it.  Short calls are latency: lengths, list, first blocks, the join.
+//   131072 rows x 4 heads, 8 query rows: 30 us a call (77.6 MB), of which 14 are fixed;
+//   32 ragged sequences x 8 heads, 4 rows, with masses: 72 us (168 MB);
+//   4096 rows x 12 heads, 1 row: 11.7 us.
+// Measured and left: eight computing warps that issue the loads in turn, 33.7 against 30.7 us for
+// each further 155 MB; two steps a warp at a time, whose chains overlap, and nine computing warps
+// with the queries in shared memory, neither faster.
 template <int D, int NT, typename T, bool kLogits>
 __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kernel(AttnArgs a) {
     constexpr int kSteps = D / 16, kRows = 8 * NT, kThreads = 32 * kWarps;

@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(256) prep_kernel(AttnArgs a) {
 // ------------------------------------------------------------------------------ masses
 // A CTA owns 128 keys of a (sequence, key head) and walks all rows, 128 at a time, through two
 // buffers in shared and tensor memory; two groups of four warps take the row tiles in turn.
-// Bound by the exponentials (one a key and row, 16 a clock and SM).
+// Bound by the exponentials (one a key and row, 16 a clock and SM: 80 us for 1560 rows x 12
+// heads x 18752 keys); it takes 141 us, six rounds of CTAs whose starts (expanding the keys)
+// only the neighbour on the SM hides.  The mma.sync form in kv4_attn.cu takes 630 us here.
 constexpr int kMassGroupThreads = 320;   // 8 warps that compute, one that loads, one that issues
 
 template <int D>
@@ -264,10 +266,17 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // A CTA (one per SM) goes through its run of the work list in segments of one (sequence, key
 // head, group of 256 rows).  Warps 0-3 and 4-7 are the softmax of the two sides (one row a
 // thread), 8-11 expand the cache (one key a thread, 128 at a time), 12 and 13 issue the products
-// of a side each, 64 keys at a time: QK of step u + 2 follows PV of step u into the same columns, so that a side's
-// softmax finds its next scores ready when it is done with the last ones.  Tensor memory: two S
-// of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its own S and is
-// the A operand of PV.  (Products of different shapes may overlap: QK waits until PV is done.)
+// of a side each, 64 keys at a time: QK of step u + 2 follows PV of step u into the same columns,
+// so that a side's softmax finds its next scores ready when it is done with the last ones.  Tensor
+// memory: two S of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its
+// own S and is the A operand of PV.  (Products of different shapes may overlap: QK waits until PV is done.)
+//
+// 1560 rows x 12 heads over 18752 rows, D = 128: 225 us for 180 GFLOP (0.80 PFLOP/s).  The
+// softmax sets the pace: of the 2300 cycles of a step (at 237 us) its warps waited 200 to 500 for
+// scores; the rest was reading them (140), hiding rows without a token (400), the maximum (220)
+// and the exponentials (1100, two warps to a scheduler).  With 128 keys a step and one S (and a
+// second sweep over it) the kernel took 307 us, with one warp issuing both sides 243, without
+// pairs 236.
 constexpr int kChunkThreads = 14 * 32;
 constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
 

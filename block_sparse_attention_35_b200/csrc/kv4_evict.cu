@@ -12,7 +12,11 @@
 // in a round, so nearly all of the work is the first, and 11 bits of a float tell octaves and
 // quarters apart, which keeps the histogram's adds off each other.  Two sweeps over the
 // registers then count and write the rows in order: the counts of a warp need no barrier, and
-// one exchange between the warps and CTAs places them.
+// one exchange between the warps and CTAs places them.  A single row (n = 1) is one reduction.
+//
+// L2 cold: 1 row of each of 32 x 8 caches of 8192 rows 7.7 us (16.8 MB, 2.2 TB/s; launch, one
+// round trip to memory and the reduction), 1560 rows of each of 12 caches of 18752 12.2 us (four
+// CTAs a cache: with one, which holds 19 keys a thread, 16.5 us).
 #include <cooperative_groups.h>
 
 #include "pbsa_device.cuh"
@@ -242,7 +246,7 @@ cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
         while (keys * ctas < tiles) ctas *= 2;
         return ctas;
     };
-    // few heads: more CTAs for each
+    // few heads: more CTAs for each, eight keys a thread
     if (tiles <= 8 * kMaxCluster && (tiles <= 8 || a.BH * cluster(8) <= kSMs)) return run<8>(a, cluster(8), 0, st);
     if (tiles <= 24 * kMaxCluster) return run<24>(a, cluster(24), 0, st);
     return run<0>(a, kMaxCluster, (tiles + kMaxCluster - 1) / kMaxCluster, st);

@@ -11,14 +11,22 @@
 // x and dy once and writes dx once; nothing is kept between them (r is a sum over a row that
 // the backward has in registers anyway).  A warp owns a token and a range of its heads: D/8
 // lanes hold one head, 8 channels (16 bytes of a 16-bit type) each, 32 / (D/8) heads per step.
-// The token's cosines and sines are loaded once and kept in registers for all of its heads,
-// and kUnroll steps of loads are issued before the first is used.  Partners of the half-split
-// pairing sit rot_dim/16 lanes away and are exchanged by shuffles, so that memory is only
-// touched with full-width accesses; interleaved partners are in the same lane.
+// The token's cosines and sines are loaded once and kept in registers for all of its heads;
+// three steps of loads are issued before the first is used, a token's first ones before its
+// position is looked up (the position, the table and the heads are then two waits, not three).
+// Partners of the half-split pairing sit rot_dim/16 lanes away and are exchanged by shuffles, so
+// that memory is only touched with full-width accesses; interleaved partners are in one lane.
 //
 // The weights' gradients stay in registers over all tokens of a warp, are summed over the
 // block in shared memory, and the blocks' sums are added by a second small kernel in a fixed
 // order (no atomics), all in 32 bits.
+//
+// 32760 tokens of 12 + 12 heads of 128 bf16 channels, three axes, L2 cold: forward 73 us
+// (403 MB, 5.5 TB/s), backward with fp32 gradients 135 us (604 MB, 4.5 TB/s: 128 registers leave
+// 16 warps an SM, and what they have in flight bounds it; with two steps of loads in flight in
+// place of three 147 us, with the weights in shared memory and the next step's loads behind this
+// step's work 152), weights' sums 3 us.
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

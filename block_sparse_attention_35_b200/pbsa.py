@@ -375,14 +375,11 @@ def _want(t, name, shape, dtype, device, strided=False):
 
 
 def _strides(*tensors):
-    """Batch, token and head strides of [B, T, H, D] tensors; NULL when all are contiguous."""
-    if all(t is None or t.is_contiguous() for t in tensors):
-        return None
-    out = (ctypes.c_int64 * (3 * len(tensors)))()
-    for i, t in enumerate(tensors):
-        if t is not None:
-            out[3 * i:3 * i + 3] = t.stride()[:3]
-    return out
+    """Batch, token and head strides of [B, T, H, D] tensors (zeros for None)."""
+    out = []
+    for t in tensors:
+        out += (0, 0, 0) if t is None else t.stride()[:3]
+    return (ctypes.c_int64 * len(out))(*out)
 
 
 # what torch.cuda.current_stream() and current_device() ask, without the objects around it
@@ -408,6 +405,12 @@ def _ok(t, shape, dtype, index):
     (These checks are most of what a call of a single token costs the host.)"""
     return (t.shape == shape and t.dtype is dtype and t.get_device() == index and
             t.is_contiguous())
+
+
+def _ok_view(t, shape, dtype, index):
+    """_ok of a strided view whose channels are contiguous."""
+    return (t.shape == shape and t.dtype is dtype and t.get_device() == index and
+            t.stride(-1) == 1)
 
 
 def _bytes(t):
@@ -456,26 +459,46 @@ def pbsa_qk_workspace_size(cfg) -> int:
 
 def _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status):
     """The quick look at what both directions share."""
-    if (q_weight is None or k_weight is None or cos is None or sin is None or pos is None or
-            status is None or not cfg.Hkv):
+    f32 = torch.float32
+    if not ((q_weight is None or _ok(q_weight, (cfg.D,), f32, i)) and
+            (k_weight is None or _ok(k_weight, (cfg.D,), f32, i)) and
+            (status is None or _ok(status, (1,), torch.int32, i))):
         return False
-    w, tab, f32 = (cfg.D,), (cfg.table_len, cfg.rot_dim // 2), torch.float32
-    return (_ok(q_weight, w, f32, i) and _ok(k_weight, w, f32, i) and _ok(cos, tab, f32, i) and
-            _ok(sin, tab, f32, i) and _ok(pos, (cfg.B, cfg.T, cfg.n_axes), torch.int32, i) and
-            _ok(status, (1,), torch.int32, i))
+    if not cfg.rot_dim:
+        return True
+    if cos is None or sin is None or pos is None or status is None:
+        return False
+    tab = (cfg.table_len, cfg.rot_dim // 2)
+    return (_ok(cos, tab, f32, i) and _ok(sin, tab, f32, i) and
+            _ok(pos, (cfg.B, cfg.T, cfg.n_axes), torch.int32, i))
+
+
+def _qk_tensors_ok(ok, cfg, i, *pairs):
+    """Whether every (query tensor, key tensor, dtype) passes `ok` (_ok or _ok_view)."""
+    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
+    for tq, tk, dt in pairs:
+        if not (ok(tq, sq, dt, i) and (not sk[2] or ok(tk, sk, dt, i))):
+            return False
+    return True
+
+
+def _own_memory(*tensors):
+    """No stride of an output is 0 (its elements would share memory)."""
+    return all(t is None or 0 not in t.stride() for t in tensors)
 
 
 def pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, pos, q_out, k_out, status,
                       stream=None):
     """RMS norm and rotation of every head; q, k, q_out, k_out may be strided views."""
     dt, i, strides = _TORCH.get(cfg.dtype), q.get_device(), None
-    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
-    if not (_qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status) and _ok(q, sq, dt, i) and
-            _ok(k, sk, dt, i) and _ok(q_out, sq, dt, i) and _ok(k_out, sk, dt, i)):
-        if not cfg.Hkv:
-            k = k_out = None
-        _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos, sin,
-                  pos, status)
+    if not cfg.Hkv:
+        k = k_out = None
+    shared = _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)
+    pairs = (q, k, dt), (q_out, k_out, dt)
+    if not (shared and _qk_tensors_ok(_ok, cfg, i, *pairs)):
+        if not (shared and _qk_tensors_ok(_ok_view, cfg, i, *pairs) and _own_memory(q_out, k_out)):
+            _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos,
+                      sin, pos, status)
         strides = _strides(q, k, q_out, k_out)
     _launch(i, stream, _lib.pbsa_qk_norm_rope, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
             _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), q_out.data_ptr(),
@@ -486,23 +509,23 @@ def pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, cos, sin, pos, dq_out, 
                           dq_weight, dk_weight, workspace, status, stream=None):
     """Gradients of pbsa_qk_norm_rope; dq_weight, dk_weight may be None."""
     dt, gt, i, strides = _TORCH.get(cfg.dtype), _TORCH.get(cfg.grad_dtype), q.get_device(), None
-    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
-    if not (_qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status) and _ok(q, sq, dt, i) and
-            _ok(k, sk, dt, i) and _ok(dq_out, sq, gt, i) and _ok(dk_out, sk, gt, i) and
-            _ok(dq, sq, dt, i) and _ok(dk, sk, dt, i)):
-        if not cfg.Hkv:
-            k = dk_out = dk = None
-        _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)),
-                  q_weight, k_weight, cos, sin, pos, status)
+    if not cfg.Hkv:
+        k = dk_out = dk = None
+    shared = _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)
+    pairs = (q, k, dt), (dq_out, dk_out, gt), (dq, dk, dt)
+    if not (shared and _qk_tensors_ok(_ok, cfg, i, *pairs)):
+        if not (shared and _qk_tensors_ok(_ok_view, cfg, i, *pairs) and _own_memory(dq, dk)):
+            _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)),
+                      q_weight, k_weight, cos, sin, pos, status)
         strides = _strides(q, k, dq_out, dk_out, dq, dk)
     for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if w is not None:
+        if w is not None and not _ok(w, (cfg.D,), torch.float32, i):
             _want(w, name, (cfg.D,), torch.float32, q.device)
     _want_workspace(workspace, q.device)
     _launch(i, stream, _lib.pbsa_qk_norm_rope_bwd, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
             _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), dq_out.data_ptr(),
-            _ptr(dk_out), dq.data_ptr(), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
-            _bytes(workspace), _ptr(status))
+            _ptr(dk_out), dq.data_ptr(), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight),
+            _ptr(workspace), _bytes(workspace), _ptr(status))
 
 
 def pbsa_validate_kv4_config(cfg):

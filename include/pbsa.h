@@ -426,7 +426,7 @@ typedef struct pbsa_kv4_cache {
     uint8_t* k_scales;  /* [B, Hkv, N, D / 16], e4m3, finite */
     uint8_t* v_codes;   /* as the keys' */
     uint8_t* v_scales;
-    int32_t* pos;       /* [B, Hkv, N]: position of the row's token, -1 = empty row */
+    int32_t* pos;       /* [B, Hkv, N]: position of the row's token (below 2^31 - 1), -1 = empty */
 } pbsa_kv4_cache;
 
 PBSA_API int pbsa_validate_kv4_config(const pbsa_kv4_config* cfg);
