@@ -55,7 +55,8 @@ int validate(const pbsa_qk_config* c) {
     if (c->B < 1 || c->T < 0) return api_failf(PBSA_ERR_ARG, "B %d must be >= 1 and T %d >= 0", c->B, c->T);
     if (c->Hq < 1 || c->Hkv < 0 || c->Hq > 65535 || c->Hkv > 65535)
         return api_failf(PBSA_ERR_ARG, "Hq %d not in [1, 65535] or Hkv %d not in [0, 65535]", c->Hq, c->Hkv);
-    if ((long long)c->B * c->T * (c->Hq + c->Hkv) > (1ll << 32))
+    const long long tokens = (long long)c->B * c->T;
+    if (tokens > (1ll << 32) || tokens * (c->Hq + c->Hkv) > (1ll << 32))
         return api_failf(PBSA_ERR_UNSUPPORTED, "more than 2^32 heads of tokens");
     if (c->D != 64 && c->D != 128) return api_failf(PBSA_ERR_UNSUPPORTED, "head dim %d: only 64 and 128 are built", c->D);
     if (c->dtype < PBSA_DTYPE_BF16 || c->dtype > PBSA_DTYPE_FP32) return api_failf(PBSA_ERR_UNSUPPORTED, "dtype %d", c->dtype);
