@@ -106,8 +106,8 @@ def test_workspace_sizes():
     (dict(axis_pairs=(64, 1)), P.PBSA_ERR_ARG), (dict(axis_pairs=(65, -1)), P.PBSA_ERR_ARG),
     (dict(grad_dtype=torch.float16), P.PBSA_ERR_UNSUPPORTED),
     (dict(B=65536, T=65536, Hq=65535), P.PBSA_ERR_UNSUPPORTED),
-    # the number of heads passes 64 bits
-    (dict(B=2 ** 31 - 1, T=2 ** 31 - 1, Hq=65535), P.PBSA_ERR_UNSUPPORTED),
+    # 65535 heads of 2^62 - 2^32 + 1 tokens: in 64 bits a negative number
+    (dict(B=2 ** 31 - 1, T=2 ** 31 - 1, Hq=65533), P.PBSA_ERR_UNSUPPORTED),
 ])
 def test_bad_head_configs_are_refused(over, code):
     kw = dict(B=1, T=4, Hq=2, Hkv=2, D=128, table_len=8)
