@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv4Args a, float inv_u
     const int pos = a.pos_new[(size_t)b * a.T + t];
     const int row = a.rows ? a.rows[bh * a.T + t] : pos;
     if (pos < 0) return;
-    if (row < 0 || row >= c.capacity) {
+    if (row < 0 || row >= c.capacity || pos == 0x7fffffff) {   // that position is kHidden
         set_status(a.status, PBSA_ERR_DEVICE_CHECK);
         return;
     }

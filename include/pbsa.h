@@ -368,8 +368,9 @@ PBSA_API size_t pbsa_qk_workspace_size(const pbsa_qk_config* cfg);
  *   q, q_out [B, T, Hq, D], k, k_out [B, T, Hkv, D] of cfg->dtype
  *   strides  NULL (all contiguous) or 12 strides in elements: batch, token and head of q, k,
  *            q_out, k_out in that order (channels are contiguous; every stride a multiple of
- *            16 bytes).  Views of one projection's output are read in place.  An output may
- *            be its own input (same pointer and strides), else they must not overlap.
+ *            16 bytes; inputs may be broadcast, with strides of 0).  Views of one projection's
+ *            output are read in place.  An output may be its own input (same pointer and
+ *            strides), else they must not overlap.
  *   wq, wk   nullable (all ones); [D] fp32
  *   cos, sin [table_len, rot_dim / 2] fp32, pos [B, T, n_axes] int32; NULL when rot_dim is 0
  *   status   device int32; a position outside [0, table_len) records PBSA_ERR_DEVICE_CHECK
@@ -415,7 +416,7 @@ PBSA_API int pbsa_qk_norm_rope_bwd(const pbsa_qk_config* cfg, const void* q, con
  */
 typedef struct pbsa_kv4_config {
     int B, Hq, Hkv, D;     /* Hq a multiple of Hkv: query head h reads key head h / (Hq / Hkv) */
-    int capacity;          /* N, rows; a multiple of 64 */
+    int capacity;          /* N, rows; a multiple of 64, at most 2^24 */
     int dtype;             /* PBSA_DTYPE_BF16 or _FP16: queries, new keys and values, outputs */
     float k_unit, v_unit;  /* powers of two in [2^-40, 2^40] */
 } pbsa_kv4_config;
@@ -441,9 +442,10 @@ PBSA_API size_t pbsa_kv4_workspace_size(const pbsa_kv4_config* cfg, int T);
  *            shorter sequence): nothing is written for it
  *   rows     nullable; [B, Hkv, T] int32, the rows to write (pbsa_kv4_evict gives them);
  *            those of one sequence and head must differ.  NULL: token at position p to row p,
- *            a cache that keeps every token.
+ *            a cache that keeps every token; the positions of one sequence must differ.
  *   mass     nullable; [B, Hkv, N] fp32: the written rows' entries become 0
- *   status   a row outside [0, N) records PBSA_ERR_DEVICE_CHECK and is skipped
+ *   status   a row outside [0, N) or a position of 2^31 - 1 records PBSA_ERR_DEVICE_CHECK and
+ *            is skipped
  */
 PBSA_API int pbsa_kv4_append(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cache,
                              const void* k_new, const void* v_new, const int64_t* strides, int T,

@@ -194,6 +194,16 @@ def test_append_padding_views_bad_rows_and_non_finite(cuda_dev):
     assert np.isfinite(c.values()[0]).all() and c.values()[0][0, 0, 0, 3] == 0
 
 
+def test_append_skips_the_last_position(cuda_dev):
+    """2^31 - 1 stands for no token inside the kernels."""
+    c = Cache(cuda_dev, B=1, Hq=1, Hkv=1, D=64, N=64)
+    k = torch.randn(1, 2, 1, 64, generator=c.g).to(torch.bfloat16).to(cuda_dev)
+    rows, pos, before = c.i32([[[3, 4]]]), c.i32([[2 ** 31 - 1, 2 ** 31 - 2]]), c.pos.clone()
+    P.pbsa_kv4_append(c.cfg, c.cache, k, k, pos, rows, None, c.status)
+    assert int(c.status.item()) == P.PBSA_ERR_DEVICE_CHECK
+    assert int(c.pos[0, 0, 3]) == int(before[0, 0, 3]) and int(c.pos[0, 0, 4]) == 2 ** 31 - 2
+
+
 # --------------------------------------------------------------------------- attention
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
@@ -431,6 +441,55 @@ def test_attention_captured_and_replayed(cuda_dev):
         mass.copy_(c.mass)
         g.replay()
         check_attention(c, q, None, n, out, lse, mass, c.mass)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunk_captured_and_replayed(cuda_dev, D):
+    """Many rows: new lengths (one of them 0), positions, queries and rows without a token."""
+    c = Cache(cuda_dev, B=2, Hq=4, Hkv=2, D=D, N=320, seed=21)
+    q, lens, q_pos = c.queries(150), c.i32([10, 20]), torch.zeros(2, 150, dtype=torch.int32, device=cuda_dev)
+    ws = torch.empty(P.pbsa_kv4_workspace_size(c.cfg, 150), dtype=torch.uint8, device=cuda_dev)
+    mass = c.mass.clone()
+    c.attend(q, q_pos, lens, mass, ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = c.attend(q, q_pos, lens, mass, ws)
+    for n in ([320, 0], [77, 300]):
+        lens.copy_(c.i32(n))
+        q.copy_(c.queries(150))
+        q_pos.copy_(torch.randint(-1, 640, (2, 150), generator=c.g, dtype=torch.int32))
+        c.pos[:, :, 5:60:7] = -1
+        mass.copy_(c.mass)
+        g.replay()
+        check_attention(c, q, q_pos, n, out, lse, mass, c.mass)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_calls_of_all_kinds_at_once(cuda_dev, D):
+    """Streams that run one row, a few and many, with masses, beside each other: every call is
+    the same as alone, bit for bit."""
+    c = Cache(cuda_dev, B=3, Hq=6, Hkv=3, D=D, N=1984, seed=22)
+    lens = c.i32([1984, 700, 0])
+    qs = [c.queries(T) for T in (1, 9, 130, 300)]
+    wss = [torch.empty(P.pbsa_kv4_workspace_size(c.cfg, q.shape[1]), dtype=torch.uint8, device=cuda_dev) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+
+    def run(q, ws):
+        mass = c.mass.clone()
+        return (*c.attend(q, None, lens, mass, ws), mass)
+
+    want = []
+    for q, ws in zip(qs, wss):
+        want.append(run(q, ws))
+        torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for q, ws, st in zip(qs, wss, streams):
+            with torch.cuda.stream(st):
+                got.append(run(q, ws))
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(r, want[i % len(qs)]))
 
 
 def test_offsets_past_32_bits(cuda_dev):
