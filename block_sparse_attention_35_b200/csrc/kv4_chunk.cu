@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // of a side each, 64 keys at a time: QK of step u + 2 follows PV of step u into the same columns,
 // so that a side's softmax finds its next scores ready when it is done with the last ones.  Tensor
 // memory: two S of 64 columns for each side, O_A, O_B; P (fp16) goes over the first half of its
-// own S and is the A operand of PV.  (Products of different shapes may overlap: QK waits until PV is done.)
+// own S and is the A operand of PV.  (Products of different shapes may overlap: QK waits until
+// PV is done.)
 //
 // 1560 rows x 12 heads over 18752 rows, D = 128: 225 us for 180 GFLOP (0.80 PFLOP/s).  The
 // softmax sets the pace: of the 2300 cycles of a step (at 237 us) its warps waited 200 to 500 for
@@ -381,14 +382,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 const Segment s = segment();
                 if (x < s.sides) {
                     const int steps = 2 * s.tiles, ends = 3 - s.sides;   // arrivals that free a tile
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&s_q[x], kTile);
-                        bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)s.bh * a.tiles128 + s.row0 / 128 + x) * kTile,
-                                  kTile, smem_u32(&s_q[x]));
+                    if (ok) {
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&s_q[x], kTile);
+                            bulk_load(smem_u32(sQ + x * kTile), a.q_tile + ((size_t)s.bh * a.tiles128 + s.row0 / 128 + x) * kTile,
+                                      kTile, smem_u32(&s_q[x]));
+                        }
+                        __syncwarp();
+                        ok = wait(&s_q[x], n_seg & 1);
+                        // after a wait that gave up: the copy may still be on its way
+                        if (!ok) mbar_wait_drain(&s_q[x], n_seg & 1, kWaitLimitNs);
                     }
-                    __syncwarp();
-                    const bool q_here = wait(&s_q[x], n_seg & 1);
-                    ok = ok && q_here;
                     const uint32_t q_lo = sdesc_lo(smem_u32(sQ + x * kTile), 16);
                     auto qk = [&](int u) {   // S of step u
                         const uint32_t t = tile + u / 2, st = t & 1;
