@@ -601,8 +601,9 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a) {
     }
 }
 
-// Groups of eight rows that a CTA of attn_kernel takes.
-int row_groups(int R) { return R <= 8 ? 1 : (R <= 16 ? 2 : 4); }
+// Groups of eight rows that a CTA of attn_kernel takes.  (20 rows x 8 heads of 4 sequences over
+// 8192 cached rows: 32.9 us with three, 37.6 with four.)
+int row_groups(int R) { return R <= 32 ? (R + 7) / 8 : 4; }
 
 bool keeps_logits(int R) { return R <= 8; }
 
@@ -671,6 +672,7 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
     if (chunk) e = launch_chunk_attn(a, st);
     else if (a.rows == 8) e = a.k.mass ? run_rows<D, 1, T, true>(a, st) : run_rows<D, 1, T, false>(a, st);
     else if (a.rows == 16) e = run_rows<D, 2, T, false>(a, st);
+    else if (a.rows == 24) e = run_rows<D, 3, T, false>(a, st);
     else e = run_rows<D, 4, T, false>(a, st);
     if (e != cudaSuccess) return e;
     const int bh = a.k.c.B * a.k.c.Hkv;

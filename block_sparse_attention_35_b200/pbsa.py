@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -146,7 +147,7 @@ def _load():
     I = ctypes.c_int
     C = ctypes.POINTER(pbsa_config)
     Z = ctypes.c_size_t
-    S = ctypes.POINTER(ctypes.c_int64)
+    S = P   # int64 strides in host memory
     QC, KC, KK = (ctypes.POINTER(t) for t in (pbsa_qk_config, pbsa_kv4_config, pbsa_kv4_cache))
     sig = {
         "pbsa_validate_config": (I, [C]),
@@ -374,12 +375,17 @@ def _want(t, name, shape, dtype, device, strided=False):
         _bad(f"{name} is not contiguous")
 
 
+def _int64s(values):
+    """An array of int64 in host memory, as a call's argument."""
+    return struct.pack(f"{len(values)}q", *values)
+
+
 def _strides(*tensors):
     """Batch, token and head strides of [B, T, H, D] tensors (zeros for None)."""
     out = []
     for t in tensors:
         out += (0, 0, 0) if t is None else t.stride()[:3]
-    return (ctypes.c_int64 * len(out))(*out)
+    return _int64s(out)
 
 
 # what torch.cuda.current_stream() and current_device() ask, without the objects around it
@@ -405,12 +411,6 @@ def _ok(t, shape, dtype, index):
     (These checks are most of what a call of a single token costs the host.)"""
     return (t.shape == shape and t.dtype is dtype and t.get_device() == index and
             t.is_contiguous())
-
-
-def _ok_view(t, shape, dtype, index):
-    """_ok of a strided view whose channels are contiguous."""
-    return (t.shape == shape and t.dtype is dtype and t.get_device() == index and
-            t.stride(-1) == 1)
 
 
 def _bytes(t):
@@ -473,32 +473,45 @@ def _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status):
             _ok(pos, (cfg.B, cfg.T, cfg.n_axes), torch.int32, i))
 
 
-def _qk_tensors_ok(ok, cfg, i, *pairs):
-    """Whether every (query tensor, key tensor, dtype) passes `ok` (_ok or _ok_view)."""
+def _qk_strides(cfg, i, *pairs):
+    """The quick look at (query tensor, key tensor, dtype) of every pair, the outputs last:
+    (True, their strides or None if all are contiguous), or (False, None) if one does not fit
+    or elements of an output may share memory."""
     sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
+    whole, tensors = True, []
     for tq, tk, dt in pairs:
-        if not (ok(tq, sq, dt, i) and (not sk[2] or ok(tk, sk, dt, i))):
-            return False
-    return True
-
-
-def _own_memory(*tensors):
-    """No stride of an output is 0 (its elements would share memory)."""
-    return all(t is None or 0 not in t.stride() for t in tensors)
+        if not (tq.shape == sq and tq.dtype is dt and tq.get_device() == i):
+            return False, None
+        tensors.append(tq)
+        whole = whole and tq.is_contiguous()
+        if tk is not None:
+            if not (tk.shape == sk and tk.dtype is dt and tk.get_device() == i):
+                return False, None
+            whole = whole and tk.is_contiguous()
+        tensors.append(tk)
+    if whole:
+        return True, None
+    out = []
+    for t in tensors:
+        st = (0, 0, 0, 1) if t is None else t.stride()
+        if st[3] != 1:
+            return False, None
+        out += st[:3]
+    if 0 in out[-6:] and any(t is not None and 0 in t.stride() for t in tensors[-2:]):
+        return False, None
+    return True, _int64s(out)
 
 
 def pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, pos, q_out, k_out, status,
                       stream=None):
     """RMS norm and rotation of every head; q, k, q_out, k_out may be strided views."""
-    dt, i, strides = _TORCH.get(cfg.dtype), q.get_device(), None
+    dt, i = _TORCH.get(cfg.dtype), q.get_device()
     if not cfg.Hkv:
         k = k_out = None
-    shared = _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)
-    pairs = (q, k, dt), (q_out, k_out, dt)
-    if not (shared and _qk_tensors_ok(_ok, cfg, i, *pairs)):
-        if not (shared and _qk_tensors_ok(_ok_view, cfg, i, *pairs) and _own_memory(q_out, k_out)):
-            _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos,
-                      sin, pos, status)
+    ok, strides = _qk_strides(cfg, i, (q, k, dt), (q_out, k_out, dt))
+    if not (ok and _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)):
+        _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos,
+                  sin, pos, status)
         strides = _strides(q, k, q_out, k_out)
     _launch(i, stream, _lib.pbsa_qk_norm_rope, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
             _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), q_out.data_ptr(),
@@ -508,15 +521,13 @@ def pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, pos, q_out, k_out
 def pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, cos, sin, pos, dq_out, dk_out, dq, dk,
                           dq_weight, dk_weight, workspace, status, stream=None):
     """Gradients of pbsa_qk_norm_rope; dq_weight, dk_weight may be None."""
-    dt, gt, i, strides = _TORCH.get(cfg.dtype), _TORCH.get(cfg.grad_dtype), q.get_device(), None
+    dt, gt, i = _TORCH.get(cfg.dtype), _TORCH.get(cfg.grad_dtype), q.get_device()
     if not cfg.Hkv:
         k = dk_out = dk = None
-    shared = _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)
-    pairs = (q, k, dt), (dq_out, dk_out, gt), (dq, dk, dt)
-    if not (shared and _qk_tensors_ok(_ok, cfg, i, *pairs)):
-        if not (shared and _qk_tensors_ok(_ok_view, cfg, i, *pairs) and _own_memory(dq, dk)):
-            _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)),
-                      q_weight, k_weight, cos, sin, pos, status)
+    ok, strides = _qk_strides(cfg, i, (q, k, dt), (dq_out, dk_out, gt), (dq, dk, dt))
+    if not (ok and _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)):
+        _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)),
+                  q_weight, k_weight, cos, sin, pos, status)
         strides = _strides(q, k, dq_out, dk_out, dq, dk)
     for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
         if w is not None and not _ok(w, (cfg.D,), torch.float32, i):
