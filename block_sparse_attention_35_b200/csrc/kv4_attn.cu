@@ -14,6 +14,7 @@ constexpr int kUnit = 16;      // keys of one tensor-core step: a warp's share o
 constexpr int kBlock = kWarps * kUnit;
 constexpr int kStages = 4;     // blocks in the ring
 constexpr int kMassWarps = 4;
+constexpr int kMassRun = 4, kMassFull = 16 * kSMs * kMassWarps;
 
 // A block of keys in shared memory, as it lies in the cache.
 template <int D>
@@ -557,47 +558,66 @@ __global__ void __launch_bounds__(kMassThreads) mass_logits_kernel(AttnArgs a) {
     *reinterpret_cast<float4*>(a.k.mass + at) = mass;
 }
 
-// Masses of many rows: the scores are formed again (half of the cache's bytes) once the rows'
-// lse is known; a warp owns its keys and walks all rows, so that every sum has one order and
-// one owner.
-template <int D>
-__global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a) {
+// Masses of up to 8 NT rows: the scores are formed again (half of the cache's bytes) once the
+// rows' lse is known; a warp owns its keys and takes all rows, so that every sum has one order
+// and one owner, and a code is turned into fp16 once.  Latency bounds it, so a warp of a large
+// call takes `run` units of keys with the next on its way (32 rows x 32 heads over 8192 cached
+// rows: 17.5 us, 22 with one unit a warp), and the first is read before the wait.
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a, int run) {
     constexpr int kSteps = D / 16;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int N = a.k.c.capacity, per_bh = N / (kUnit * kMassWarps);
+    const int N = a.k.c.capacity, units = N / kUnit, per_bh = (units + kMassWarps * run - 1) / (kMassWarps * run);
     const int bh = blockIdx.x / per_bh, b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv;
+    const int len = used_rows(a, b), used = (len + kUnit - 1) / kUnit;
+    int u = (blockIdx.x % per_bh) * kMassWarps * run + warp;
+    const int end = min(used, u + kMassWarps * run);
+    const size_t row0 = (size_t)bh * N;
+    auto load = [&](Keys<D>& x, int unit) {
+        const size_t row = row0 + (size_t)unit * kUnit;
+        load_keys(x, a.k.cache.k_codes + row * (D / 2), a.k.cache.k_scales + row * (D / 16), a.k.cache.pos + row, lane);
+    };
+    Keys<D> x;   // the first is read while the kernels before still run
+    if (u < end) load(x, u);
     grid_dependency_wait();
-    const int u = (blockIdx.x % per_bh) * kMassWarps + warp;
-    const int len = used_rows(a, b);
-    if (u * kUnit >= len) return;
-    Keys<D> x;
-    const size_t row0 = (size_t)bh * N + (size_t)u * kUnit;
-    load_keys(x, a.k.cache.k_codes + row0 * (D / 2), a.k.cache.k_scales + row0 * (D / 16), a.k.cache.pos + row0, lane);
-    hide_keys(x, len - u * kUnit, lane);
-    float sum[2] = {0.f, 0.f};
-    for (int tile = 0; tile < a.tiles8; ++tile) {
-        const size_t at = (size_t)bh * a.tiles8 + tile;
-        uint2 f[kSteps];
+    if (u >= end) return;
+    const uint2* q = a.q_frag + (size_t)bh * NT * kSteps * 32 + lane;
+    float fac[NT][2], lse[NT][2];
+    int lim[NT][2];
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) f[j] = a.q_frag[(at * kSteps + j) * 32 + lane];
-        float s[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-        scores<D, 1>(s, x, [&](int j, int) { return f[j]; });
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = tile * 8 + 2 * c + i, rr = min(r, a.R - 1);
-            const int lim = row_limit(a, b, r);
-            const float fac = a.q_fac[at * 8 + 2 * c + i];
-            const float lse = a.k.lse[((size_t)b * a.k.c.Hq + hkv * a.G + rr % a.G) * a.k.T + rr / a.G] * kLog2e;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (x.pos[k] <= lim) sum[k] += ex2(s[0][i + 2 * k] * fac - lse);
+            const int r = 8 * n + 2 * c + i, rr = min(r, a.R - 1);
+            lim[n][i] = row_limit(a, b, r);
+            fac[n][i] = a.q_fac[((size_t)bh * NT + n) * 8 + 2 * c + i];
+            lse[n][i] = a.k.lse[((size_t)b * a.k.c.Hq + hkv * a.G + rr % a.G) * a.k.T + rr / a.G] * kLog2e;
         }
-    }
+    for (; u < end; u += kMassWarps) {
+        const int unit = u;
+        Keys<D> y = x;
+        if (u + kMassWarps < end) load(x, u + kMassWarps);
+        hide_keys(y, len - unit * kUnit, lane);
+        float s[NT][4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-        if (c == 0 && x.pos[k] != kHidden) a.k.mass[row0 + g + 8 * k] += sum[k];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+        scores<D, NT>(s, y, [&](int j, int n) { return q[(n * kSteps + j) * 32]; });
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (y.pos[k] <= lim[n][i]) sum[k] += ex2(s[n][i + 2 * k] * fac[n][i] - lse[n][i]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+            if (c == 0 && y.pos[k] != kHidden) a.k.mass[row0 + (size_t)unit * kUnit + g + 8 * k] += sum[k];
+        }
     }
 }
 
@@ -692,8 +712,13 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
         const unsigned runs = (unsigned)((a.k.c.capacity + 4 * kMassThreads - 1) / (4 * kMassThreads));
         return launch_after(mass_logits_kernel, dim3((unsigned)bh, runs), kMassThreads, 0, st, a);
     }
-    return launch_after(mass_kernel<D>, dim3((unsigned)(bh * (a.k.c.capacity / (kUnit * kMassWarps)))),
-                        32 * kMassWarps, 0, st, a);
+    // units of sixteen keys that a warp takes: several where all of them fill the GPU
+    const int units = a.k.c.capacity / kUnit, run = (long long)bh * units >= kMassFull ? kMassRun : 1;
+    const dim3 grid((unsigned)(bh * ((units + kMassWarps * run - 1) / (kMassWarps * run))));
+    auto mass = [&](auto kernel) { return launch_after(kernel, grid, 32 * kMassWarps, 0, st, a, run); };
+    if (a.tiles8 == 2) return mass(mass_kernel<D, 2>);
+    if (a.tiles8 == 3) return mass(mass_kernel<D, 3>);
+    return mass(mass_kernel<D, 4>);
 }
 
 }  // namespace

@@ -210,7 +210,9 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int b, int hkv, in
 
 // Launches a kernel that may start while the one before it in the stream still runs; every
 // thread of it waits for that one (grid_dependency_wait) before it reads its results.
-inline cudaError_t launch_after(void (*kernel)(AttnArgs), dim3 grid, int threads, size_t smem, cudaStream_t st, const AttnArgs& a) {
+template <typename... More>
+cudaError_t launch_after(void (*kernel)(AttnArgs, More...), dim3 grid, int threads, size_t smem, cudaStream_t st, const AttnArgs& a,
+                         More... more) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -221,7 +223,7 @@ inline cudaError_t launch_after(void (*kernel)(AttnArgs), dim3 grid, int threads
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, more...);
 }
 
 // Many rows (kv4_chunk.cu): whether it takes a call, and its launches.

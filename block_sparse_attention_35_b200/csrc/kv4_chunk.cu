@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
 }  // namespace
 
 // With 32 rows (4 sequences x 8 heads, 8192 cached rows) attn_kernel takes 39.5 us and
-// chunk_kernel 39.8 (63 against 74 with masses); with 40 rows, of which attn_kernel needs two
+// chunk_kernel 39.8 (57 against 74 with masses); with 40 rows, of which attn_kernel needs two
 // groups, 56.6 against 40.3 (85 against 75).
 bool chunk_takes(int R) { return R > 32; }
 

@@ -336,6 +336,17 @@ def test_long_splits_join(cuda_dev):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("D,T,Hq", [(64, 3, 4), (128, 5, 4), (64, 4, 8)])
+def test_masses_of_many_cached_rows(cuda_dev, D, T, Hq):
+    """Enough rows that a warp of the mass kernel takes several units; lengths end inside them."""
+    c = Cache(cuda_dev, B=3, Hq=Hq, Hkv=1, D=D, N=51200, seed=23)
+    lens, q = [51200, 20011, 1], c.queries(T)
+    q_pos = torch.randint(30000, 90000, (3, T), generator=c.g, dtype=torch.int32).to(cuda_dev)
+    mass = c.mass.clone()
+    out, lse = c.attend(q, q_pos, c.i32(lens), mass)
+    check_attention(c, q, q_pos, lens, out, lse, mass, c.mass)
+
+
 def test_causal_steps_equal_single_tokens(cuda_dev):
     """T tokens under the causal mask give what they give one at a time."""
     N, T = 128, 6
