@@ -9,8 +9,8 @@
 //                128 rows, ready for one bulk copy each.
 //  chunk_kernel  S = Q K^T, online softmax, O += P V for 256 rows a CTA (two sides of 128);
 //                CTAs split the work list as attn_kernel's do and join_kernel joins them.
-//  mass_kernel   S^T = K Q^T with the rows' final lse: a lane of tensor memory is a key, so a
-//                key's mass is a sum along one thread's columns, with one owner and one order.
+//  chunk_mass_kernel  S^T = K Q^T with the rows' final lse: a lane of tensor memory is a key, so
+//                a key's mass is a sum along four threads' columns, with one owner and one order.
 #include "kv4_attn.cuh"
 
 namespace pbsa {
@@ -64,6 +64,17 @@ __device__ __forceinline__ void expand32(uint8_t* tile, int row, int q, const ui
     }
 }
 
+// 16 lanes x 32 columns of tensor memory, as products of mma.sync lie: lane 4 g + c gets, of
+// columns 8 j + 2 c and the next one, rows g (d[4 j], d[4 j + 1]) and g + 8 (d[4 j + 2], ..).
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t addr, uint32_t (&d)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7]), "=r"(d[8]),
+          "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]), "=r"(d[13]), "=r"(d[14]), "=r"(d[15])
+        : "r"(addr));
+}
+
 // One warp per query row; D / 4 lanes hold it, four channels each.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) prep_kernel(AttnArgs a) {
@@ -84,9 +95,14 @@ __global__ void __launch_bounds__(256) prep_kernel(AttnArgs a) {
 // ------------------------------------------------------------------------------ masses
 // A CTA owns 128 keys of a (sequence, key head) and walks all rows, 128 at a time, through two
 // buffers in shared and tensor memory; two groups of four warps take the row tiles in turn.
+// Tensor memory is read as products of mma.sync lie, four keys and a quarter of the columns a
+// lane: the columns' factors and lse cost a quarter of the shared-memory loads that a lane per
+// key would take (141 against 138 us).
 // Bound by the exponentials (one a key and row, 16 a clock and SM: 80 us for 1560 rows x 12
-// heads x 18752 keys); it takes 141 us, six rounds of CTAs whose starts (expanding the keys)
-// only the neighbour on the SM hides.  The mma.sync form in kv4_attn.cu takes 630 us here.
+// heads x 18752 keys); it takes 138 us: 8.8 us for each 128 rows (73 % of that rate) and 23 for
+// the starts of six rounds of CTAs (expanding the keys).  A quarter of the exponentials as
+// polynomials on the FMA pipe changed nothing, here and in chunk_kernel; half of them cost 17 us
+// here and 13 there.  The mma.sync form that preceded it took 630 us.
 constexpr int kMassGroupThreads = 320;   // 8 warps that compute, one that loads, one that issues
 
 template <int D>
@@ -101,6 +117,7 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
     __shared__ __align__(16) float s_col[2][2][64][4];
     __shared__ int s_lim[2][2][128];
     __shared__ float s_sum[128];
+    __shared__ int s_pos[128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int N = a.k.c.capacity, per = (N + 127) / 128, bh = blockIdx.x / per, key0 = (blockIdx.x % per) * 128;
@@ -123,8 +140,8 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
         fence_barrier_init();
     }
     if (warp == 9) tmem_alloc(&s_tmem, 256);
-    int pos = kHidden;   // of this thread's key (compute warps: lane of tensor memory)
     if (warp < 8) {
+        int pos = kHidden;
         // two threads to a key, each half of its channels
         const int key = tid & 127, part = tid >> 7;
         const size_t row = (size_t)bh * N + key0 + key;
@@ -141,6 +158,7 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
             }
             expand32(sK, key, q, codes, sc);
         }
+        if (part == 0) s_pos[key] = pos;
         fence_proxy_async_smem();
     }
     grid_dependency_wait();
@@ -195,7 +213,14 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
     } else {
         const int group = warp >> 2, key = tid & 127;
         const uint32_t addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * group;
-        float sum = 0.f;
+        // this thread's keys: k0 + 16 h + 8 i, of which it takes every fourth pair of columns
+        const int k0 = (warp & 3) * 32 + (lane >> 2), c4 = lane & 3;
+        int pos[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pos[h][i] = s_pos[k0 + 16 * h + 8 * i];
+        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
         bool ok = true;
         // a row's column: its factor, lse and limit; thread i prepares column i of the next tile
         auto column = [&](int t) -> float4 {
@@ -220,39 +245,70 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status));
             if (ok) {
                 tc_fence_after();
-                uint64_t part[2] = {0, 0};
+                uint64_t part[2][2] = {{0, 0}, {0, 0}};
                 uint32_t u[2][16];
-                tmem_ld16(addr, u[0]);
+                float4 col[4];
+                int2 lim[4];
+                tmem_ld_rows16(addr, u[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int k = 0; k < 8; ++k) {   // 32 columns, 16 keys
+                    const int h = k & 1, c0 = (k >> 1) * 32;
                     tmem_ld_wait();
-                    if (c < 7) {
-                        tmem_ld16(addr + 16 * (c + 1), u[(c + 1) & 1]);
+                    if (k < 7) {
+                        tmem_ld_rows16(addr + ((k + 1) >> 1) * 32 + (static_cast<uint32_t>(((k + 1) & 1) * 16) << 16), u[(k + 1) & 1]);
                     } else {
                         tc_fence_before();
                         mbar_arrive(&s_free[group]);
                     }
+                    if (h == 0) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float4 col = *reinterpret_cast<const float4*>(s_col[group][buf][8 * c + e / 2]);
-                        float2 x = split(fma2(pair(__uint_as_float(u[c & 1][e]), __uint_as_float(u[c & 1][e + 1])),
-                                              pair(col.x, col.y), pair(col.z, col.w)));
-                        x.x = ex2(x.x), x.y = ex2(x.y);
-                        if (a.k.q_pos) {
-                            const int2 lim = *reinterpret_cast<const int2*>(&s_lim[group][buf][16 * c + e]);
-                            x.x = pos <= lim.x ? x.x : 0.f;
-                            x.y = pos <= lim.y ? x.y : 0.f;
+                        for (int j = 0; j < 4; ++j) {
+                            col[j] = *reinterpret_cast<const float4*>(s_col[group][buf][c0 / 2 + 4 * j + c4]);
+                            if (a.k.q_pos) lim[j] = *reinterpret_cast<const int2*>(&s_lim[group][buf][c0 + 8 * j + 2 * c4]);
                         }
-                        part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pair(x.x, x.y));
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float2 x = split(fma2(pair(__uint_as_float(u[k & 1][4 * j + 2 * i]), __uint_as_float(u[k & 1][4 * j + 2 * i + 1])),
+                                                  pair(col[j].x, col[j].y), pair(col[j].z, col[j].w)));
+                            x.x = ex2(x.x), x.y = ex2(x.y);
+                            if (a.k.q_pos) {
+                                x.x = pos[h][i] <= lim[j].x ? x.x : 0.f;
+                                x.y = pos[h][i] <= lim[j].y ? x.y : 0.f;
+                            }
+                            part[h][i] = add2(part[h][i], pair(x.x, x.y));
+                        }
                 }
-                const float2 sums = split(add2(part[0], part[1]));
-                sum += sums.x + sums.y;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 sums = split(part[h][i]);
+                        sum[h][i] += sums.x + sums.y;
+                    }
             }
         }
-        if (group == 1) s_sum[key] = sum;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sum[h][i] += __shfl_xor_sync(0xffffffffu, sum[h][i], 1);
+                sum[h][i] += __shfl_xor_sync(0xffffffffu, sum[h][i], 2);
+                if (group == 1 && c4 == 0) s_sum[k0 + 16 * h + 8 * i] = sum[h][i];
+            }
         named_bar_sync(3, 256);
-        if (group == 0 && ok && pos != kHidden) a.k.mass[(size_t)bh * N + key0 + key] += sum + s_sum[key];
+        if (group == 0 && c4 == 0 && ok) {
+            float* mass = a.k.mass + (size_t)bh * N + key0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int kk = k0 + 16 * h + 8 * i;
+                    if (pos[h][i] != kHidden) mass[kk] += sum[h][i] + s_sum[kk];
+                }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -277,7 +333,7 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // scores; the rest was reading them (140), hiding rows without a token (400), the maximum (220)
 // and the exponentials (1100, two warps to a scheduler).  With 128 keys a step and one S (and a
 // second sweep over it) the kernel took 307 us, with one warp issuing both sides 243, without
-// pairs 236.
+// pairs 236.  A last group of at most 128 rows takes nearly as long as a whole one (29 us each).
 constexpr int kChunkThreads = 14 * 32;
 constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
 
