@@ -1,13 +1,17 @@
-"""Builds libpbsa.so (the C ABI of include/pbsa.h) in-tree for sm_100a with nvcc."""
+"""Builds, in-tree, libpbsa.so (the C ABI of include/pbsa.h) for sm_100a with nvcc and
+token_calls.so (a CPython module over torch's tensors) with the host compiler."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libpbsa.so")
+CALLS = os.path.join(PKG, "token_calls.so")
+CALLS_SOURCE = os.path.join(PKG, "csrc", "token_calls.cpp")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-shared", "--threads", "0", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -22,14 +26,27 @@ def headers():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in sources() + headers())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    return all(os.path.getmtime(f) <= t for f in sources() + headers() + [CALLS_SOURCE])
+
+
+def calls_command():
+    import torch
+    from torch.utils import cpp_extension
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I", os.path.join(ROOT, "include"), *(x for d in includes for x in ("-isystem", d)),
+            "-o", CALLS + ".tmp", CALLS_SOURCE, "-L", PKG, "-lpbsa",
+            *(x for d in cpp_extension.library_paths() for x in ("-L", d)),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ into one shared library; returns its path."""
+    """Compile every .cu under csrc/ into one shared library, and the module beside it; returns
+    the library's path."""
     if not force and up_to_date():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -38,6 +55,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    cmd = calls_command()
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 

@@ -11,7 +11,6 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-import struct
 
 import torch
 
@@ -142,12 +141,12 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python -m block_sparse_attention_35_b200.build`")
-    lib = ctypes.CDLL(LIB_PATH)
+    lib = ctypes.CDLL(LIB_PATH)   # before token_calls, which is linked with it
     P = ctypes.c_void_p
     I = ctypes.c_int
     C = ctypes.POINTER(pbsa_config)
     Z = ctypes.c_size_t
-    S = P   # int64 strides in host memory
+    S = ctypes.POINTER(ctypes.c_int64)
     QC, KC, KK = (ctypes.POINTER(t) for t in (pbsa_qk_config, pbsa_kv4_config, pbsa_kv4_cache))
     sig = {
         "pbsa_validate_config": (I, [C]),
@@ -188,6 +187,8 @@ def _load():
 
 
 _lib = _load()
+
+from . import token_calls as _calls  # noqa: E402  (built with the library)
 
 
 def header_symbols(path: str = HEADER):
@@ -354,7 +355,9 @@ def pbsa_select_blocks_noalloc(cfg, q, q_frames, k_local, local_frames, ring_hea
 
 # --------------------------------------------- token operators: heads and the 4-bit cache
 # These calls check what a pointer cannot show - shapes, types, the device - before they hand
-# the pointers on, and run on the current stream of the tensors' device.
+# the pointers on, and run on the current stream of the tensors' device.  Where all is as it
+# should be and that device is the current one, csrc/token_calls.cpp makes them; what it leaves
+# alone is checked here, with an error that says what does not fit.
 
 def _bad(msg):
     raise PBSAError(PBSA_ERR_ARG, msg)
@@ -375,17 +378,13 @@ def _want(t, name, shape, dtype, device, strided=False):
         _bad(f"{name} is not contiguous")
 
 
-def _int64s(values):
-    """An array of int64 in host memory, as a call's argument."""
-    return struct.pack(f"{len(values)}q", *values)
-
-
 def _strides(*tensors):
-    """Batch, token and head strides of [B, T, H, D] tensors (zeros for None)."""
+    """Batch, token and head strides of [B, T, H, D] tensors (zeros for None, and where there is
+    one element: its stride says nothing)."""
     out = []
     for t in tensors:
-        out += (0, 0, 0) if t is None else t.stride()[:3]
-    return _int64s(out)
+        out += (0, 0, 0) if t is None else (0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()))
+    return (ctypes.c_int64 * len(out))(*out)
 
 
 # what torch.cuda.current_stream() and current_device() ask, without the objects around it
@@ -406,11 +405,17 @@ def _launch(index, stream, call, *args):
         _check(rc)
 
 
-def _ok(t, shape, dtype, index):
-    """Whether a tensor is as it nearly always is; the caller looks closer where it is not.
-    (These checks are most of what a call of a single token costs the host.)"""
-    return (t.shape == shape and t.dtype is dtype and t.get_device() == index and
-            t.is_contiguous())
+def _quick(call, kind, cfg, index, stream, *args):
+    """Makes an ordinary call through token_calls; False if it is not one."""
+    if index < 0 or type(cfg) is not kind or _current_device() != index:
+        return False
+    rc = call(ctypes.addressof(cfg), index, _raw_stream(index) if stream is None else _stream(stream),
+              *args)
+    if rc is None:
+        return False
+    if rc != PBSA_OK:
+        _check(rc)
+    return True
 
 
 def _bytes(t):
@@ -457,84 +462,41 @@ def pbsa_qk_workspace_size(cfg) -> int:
     return n
 
 
-def _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status):
-    """The quick look at what both directions share."""
-    f32 = torch.float32
-    if not ((q_weight is None or _ok(q_weight, (cfg.D,), f32, i)) and
-            (k_weight is None or _ok(k_weight, (cfg.D,), f32, i)) and
-            (status is None or _ok(status, (1,), torch.int32, i))):
-        return False
-    if not cfg.rot_dim:
-        return True
-    if cos is None or sin is None or pos is None or status is None:
-        return False
-    tab = (cfg.table_len, cfg.rot_dim // 2)
-    return (_ok(cos, tab, f32, i) and _ok(sin, tab, f32, i) and
-            _ok(pos, (cfg.B, cfg.T, cfg.n_axes), torch.int32, i))
-
-
-def _qk_strides(cfg, i, *pairs):
-    """The quick look at (query tensor, key tensor, dtype) of every pair, the outputs last:
-    (True, their strides or None if all are contiguous), or (False, None) if one does not fit
-    or elements of an output may share memory."""
-    sq, sk = (cfg.B, cfg.T, cfg.Hq, cfg.D), (cfg.B, cfg.T, cfg.Hkv, cfg.D)
-    whole, tensors = True, []
-    for tq, tk, dt in pairs:
-        if not (tq.shape == sq and tq.dtype is dt and tq.get_device() == i):
-            return False, None
-        tensors.append(tq)
-        whole = whole and tq.is_contiguous()
-        if tk is not None:
-            if not (tk.shape == sk and tk.dtype is dt and tk.get_device() == i):
-                return False, None
-            whole = whole and tk.is_contiguous()
-        tensors.append(tk)
-    if whole:
-        return True, None
-    out = []
-    for t in tensors:
-        st = (0, 0, 0, 1) if t is None else t.stride()
-        if st[3] != 1:
-            return False, None
-        out += st[:3]
-    if 0 in out[-6:] and any(t is not None and 0 in t.stride() for t in tensors[-2:]):
-        return False, None
-    return True, _int64s(out)
-
-
 def pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, pos, q_out, k_out, status,
                       stream=None):
     """RMS norm and rotation of every head; q, k, q_out, k_out may be strided views."""
-    dt, i = _TORCH.get(cfg.dtype), q.get_device()
+    i = q.get_device()
+    if _quick(_calls.qk_norm_rope, pbsa_qk_config, cfg, i, stream, q, k, q_weight, k_weight, cos, sin,
+              pos, q_out, k_out, status):
+        return
+    dt = _TORCH.get(cfg.dtype)
     if not cfg.Hkv:
         k = k_out = None
-    ok, strides = _qk_strides(cfg, i, (q, k, dt), (q_out, k_out, dt))
-    if not (ok and _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)):
-        _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos,
-                  sin, pos, status)
-        strides = _strides(q, k, q_out, k_out)
-    _launch(i, stream, _lib.pbsa_qk_norm_rope, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
-            _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), q_out.data_ptr(),
+    _qk_check(cfg, (("", q, k, dt), ("_out", q_out, k_out, dt)), q_weight, k_weight, cos, sin, pos,
+              status)
+    _launch(i, stream, _lib.pbsa_qk_norm_rope, _cfg(cfg), q.data_ptr(), _ptr(k),
+            _strides(q, k, q_out, k_out), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), q_out.data_ptr(),
             _ptr(k_out), _ptr(status))
 
 
 def pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, cos, sin, pos, dq_out, dk_out, dq, dk,
                           dq_weight, dk_weight, workspace, status, stream=None):
     """Gradients of pbsa_qk_norm_rope; dq_weight, dk_weight may be None."""
-    dt, gt, i = _TORCH.get(cfg.dtype), _TORCH.get(cfg.grad_dtype), q.get_device()
+    i = q.get_device()
+    if _quick(_calls.qk_norm_rope_bwd, pbsa_qk_config, cfg, i, stream, q, k, q_weight, k_weight, cos,
+              sin, pos, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, status):
+        return
+    dt, gt = _TORCH.get(cfg.dtype), _TORCH.get(cfg.grad_dtype)
     if not cfg.Hkv:
         k = dk_out = dk = None
-    ok, strides = _qk_strides(cfg, i, (q, k, dt), (dq_out, dk_out, gt), (dq, dk, dt))
-    if not (ok and _qk_ok(cfg, i, q_weight, k_weight, cos, sin, pos, status)):
-        _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)),
-                  q_weight, k_weight, cos, sin, pos, status)
-        strides = _strides(q, k, dq_out, dk_out, dq, dk)
+    _qk_check(cfg, (("", q, k, dt), ("d_out", dq_out, dk_out, gt), ("d", dq, dk, dt)), q_weight,
+              k_weight, cos, sin, pos, status)
     for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if w is not None and not _ok(w, (cfg.D,), torch.float32, i):
+        if w is not None:
             _want(w, name, (cfg.D,), torch.float32, q.device)
     _want_workspace(workspace, q.device)
-    _launch(i, stream, _lib.pbsa_qk_norm_rope_bwd, _cfg(cfg), q.data_ptr(), _ptr(k), strides,
-            _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), dq_out.data_ptr(),
+    _launch(i, stream, _lib.pbsa_qk_norm_rope_bwd, _cfg(cfg), q.data_ptr(), _ptr(k),
+            _strides(q, k, dq_out, dk_out, dq, dk), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(pos), dq_out.data_ptr(),
             _ptr(dk_out), dq.data_ptr(), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight),
             _ptr(workspace), _bytes(workspace), _ptr(status))
 
@@ -559,33 +521,34 @@ def _kv4_check(cfg, cache):
 def pbsa_kv4_append(cfg, cache, k_new, v_new, pos_new, rows, mass, status, stream=None):
     """Quantises the new tokens' keys and values into `rows` (None: row = position)."""
     dev, i = _kv4_check(cfg, cache)
+    if _quick(_calls.kv4_append, pbsa_kv4_config, cfg, i, stream, ctypes.addressof(cache), k_new, v_new,
+              pos_new, rows, mass, status):
+        return
     B, Hkv, T, dt, i32 = cfg.B, cfg.Hkv, k_new.shape[1], _TORCH.get(cfg.dtype), torch.int32
-    strides, shape = None, (B, T, Hkv, cfg.D)
-    if not (_ok(k_new, shape, dt, i) and _ok(v_new, shape, dt, i) and
-            _ok(pos_new, (B, T), i32, i) and _ok(status, (1,), i32, i)):
-        _want(k_new, "k_new", shape, dt, dev, True)
-        _want(v_new, "v_new", shape, dt, dev, True)
-        _want(pos_new, "pos_new", (B, T), i32, dev)
-        _want(status, "status", (1,), i32, dev)
-        strides = _strides(k_new, v_new)
+    shape = (B, T, Hkv, cfg.D)
+    _want(k_new, "k_new", shape, dt, dev, True)
+    _want(v_new, "v_new", shape, dt, dev, True)
+    _want(pos_new, "pos_new", (B, T), i32, dev)
+    _want(status, "status", (1,), i32, dev)
     if rows is not None:
         _want(rows, "rows", (B, Hkv, T), i32, dev)
     if mass is not None:
         _want(mass, "mass", (B, Hkv, cfg.capacity), torch.float32, dev)
     _launch(i, stream, _lib.pbsa_kv4_append, _cfg(cfg), ctypes.byref(cache), k_new.data_ptr(),
-            v_new.data_ptr(), strides, T, pos_new.data_ptr(), _ptr(rows), _ptr(mass), _ptr(status))
+            v_new.data_ptr(), _strides(k_new, v_new), T, pos_new.data_ptr(), _ptr(rows), _ptr(mass), _ptr(status))
 
 
 def pbsa_kv4_read(cfg, cache, rows, k_out, v_out, status, stream=None):
     """The values of the given rows (None: the first k_out.shape[2] rows)."""
     dev, i = _kv4_check(cfg, cache)
+    if _quick(_calls.kv4_read, pbsa_kv4_config, cfg, i, stream, ctypes.addressof(cache), rows, k_out,
+              v_out, status):
+        return
     n, dt = k_out.shape[2], _TORCH.get(cfg.dtype)
     shape = (cfg.B, cfg.Hkv, n, cfg.D)
-    if not (_ok(k_out, shape, dt, i) and _ok(v_out, shape, dt, i) and
-            _ok(status, (1,), torch.int32, i)):
-        _want(k_out, "k_out", shape, dt, dev)
-        _want(v_out, "v_out", shape, dt, dev)
-        _want(status, "status", (1,), torch.int32, dev)
+    _want(k_out, "k_out", shape, dt, dev)
+    _want(v_out, "v_out", shape, dt, dev)
+    _want(status, "status", (1,), torch.int32, dev)
     if rows is not None:
         _want(rows, "rows", shape[:3], torch.int32, dev)
     _launch(i, stream, _lib.pbsa_kv4_read, _cfg(cfg), ctypes.byref(cache), _ptr(rows), n,
@@ -595,38 +558,39 @@ def pbsa_kv4_read(cfg, cache, rows, k_out, v_out, status, stream=None):
 def pbsa_kv4_attn(cfg, cache, q, q_pos, kv_len, out, lse, mass, workspace, status, stream=None):
     """Attention of q [B, T, Hq, D] over the cache; q_pos and mass may be None."""
     dev, i = _kv4_check(cfg, cache)
+    if _quick(_calls.kv4_attn, pbsa_kv4_config, cfg, i, stream, ctypes.addressof(cache), q, q_pos,
+              kv_len, out, lse, mass, workspace, status):
+        return
     B, Hq, T, dt = cfg.B, cfg.Hq, q.shape[1], _TORCH.get(cfg.dtype)
-    f32, i32, strides, shape = torch.float32, torch.int32, None, (B, T, Hq, cfg.D)
-    if not (_ok(q, shape, dt, i) and _ok(out, shape, dt, i) and _ok(lse, (B, Hq, T), f32, i) and
-            _ok(kv_len, (B,), i32, i) and _ok(status, (1,), i32, i)):
-        _want(q, "q", shape, dt, dev, True)
-        _want(out, "out", shape, dt, dev)
-        _want(lse, "lse", (B, Hq, T), f32, dev)
-        _want(kv_len, "kv_len", (B,), i32, dev)
-        _want(status, "status", (1,), i32, dev)
-        strides = _strides(q)
+    f32, i32, shape = torch.float32, torch.int32, (B, T, Hq, cfg.D)
+    _want(q, "q", shape, dt, dev, True)
+    _want(out, "out", shape, dt, dev)
+    _want(lse, "lse", (B, Hq, T), f32, dev)
+    _want(kv_len, "kv_len", (B,), i32, dev)
+    _want(status, "status", (1,), i32, dev)
     if q_pos is not None:
         _want(q_pos, "q_pos", (B, T), i32, dev)
     if mass is not None:
         _want(mass, "mass", (B, cfg.Hkv, cfg.capacity), f32, dev)
     _want_workspace(workspace, dev)
-    _launch(i, stream, _lib.pbsa_kv4_attn, _cfg(cfg), ctypes.byref(cache), q.data_ptr(), strides, T,
+    _launch(i, stream, _lib.pbsa_kv4_attn, _cfg(cfg), ctypes.byref(cache), q.data_ptr(), _strides(q), T,
             _ptr(q_pos), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(mass), _ptr(workspace),
             _bytes(workspace), _ptr(status))
 
 
 def pbsa_kv4_evict(cfg, pos, mass, n_sink, keep_from, rows, status, stream=None):
     """Chooses rows.shape[2] rows of every sequence and key head for the next tokens."""
-    i, n, i32 = pos.get_device(), rows.shape[2], torch.int32
+    i = pos.get_device()
+    if _quick(_calls.kv4_evict, pbsa_kv4_config, cfg, i, stream, pos, mass, n_sink, keep_from, rows,
+              status):
+        return
+    n, i32, dev = rows.shape[2], torch.int32, pos.device
     B, Hkv = cfg.B, cfg.Hkv
     shape = (B, Hkv, cfg.capacity)
-    if not (_ok(pos, shape, i32, i) and _ok(mass, shape, torch.float32, i) and
-            _ok(rows, (B, Hkv, n), i32, i) and _ok(status, (1,), i32, i)):
-        dev = pos.device
-        _want(pos, "pos", shape, i32, dev)
-        _want(mass, "mass", shape, torch.float32, dev)
-        _want(rows, "rows", (B, Hkv, n), i32, dev)
-        _want(status, "status", (1,), i32, dev)
+    _want(pos, "pos", shape, i32, dev)
+    _want(mass, "mass", shape, torch.float32, dev)
+    _want(rows, "rows", (B, Hkv, n), i32, dev)
+    _want(status, "status", (1,), i32, dev)
     if keep_from is not None:
         _want(keep_from, "keep_from", (B,), i32, pos.device)
     _launch(i, stream, _lib.pbsa_kv4_evict, _cfg(cfg), _ptr(pos), _ptr(mass), n, n_sink,

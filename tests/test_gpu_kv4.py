@@ -662,6 +662,31 @@ def test_generation_with_a_bounded_cache(cuda_dev, graph):
     assert tc.seen.tolist() == [78, 59]
 
 
+def test_calls_refuse_tensors_that_do_not_fit(cuda_dev):
+    c = Cache(cuda_dev, B=2, Hq=4, Hkv=2, D=64, N=128)
+    bf = dict(dtype=torch.bfloat16, device=cuda_dev)
+    rows, pos = torch.zeros(2, 2, 1, dtype=torch.int32, device=cuda_dev), c.i32([[1], [2]])
+    kv, out = torch.zeros(2, 1, 2, 64, **bf), torch.zeros(2, 2, 1, 64, **bf)
+    ws = torch.empty(P.pbsa_kv4_workspace_size(c.cfg, 1), dtype=torch.uint8, device=cuda_dev)
+    calls = [
+        (P.pbsa_kv4_append, [kv, kv.clone(), pos, rows, c.mass, c.status], (3, 4)),
+        (P.pbsa_kv4_read, [rows, out, out.clone(), c.status], (0,)),
+        (P.pbsa_kv4_attn, [c.queries(1), pos, c.i32([5, 6]), torch.zeros(2, 1, 4, 64, **bf),
+                           torch.zeros(2, 4, 1, device=cuda_dev), c.mass, ws, c.status], (1, 5)),
+        (lambda cfg, cache, *a: P.pbsa_kv4_evict(cfg, a[0], a[1], 0, *a[2:]), [c.pos, c.mass, c.i32([0, 0]), rows, c.status], (2,)),
+    ]
+    before = [x.clone() for x in (c.kc, c.ks, c.vc, c.vs, c.pos, c.mass, rows, out)]
+    for call, args, may_be_none in calls:
+        for i, x in enumerate(args):
+            # (a longer or wider workspace, a batch of one more dimension of new tokens fit)
+            bad = [x.cpu()] if x is ws else [x.cpu(), x.double(), x[None], x.expand(3, *x.shape[1:]) if x.shape[0] == 1 else x[:1]]
+            for y in bad + ([] if i in may_be_none else [None]):
+                with pytest.raises((P.PBSAError, AttributeError)):
+                    call(c.cfg, c.cache, *args[:i], y, *args[i + 1:])
+    assert int(c.status.item()) == 0
+    assert all(torch.equal(x, y) for x, y in zip(before, (c.kc, c.ks, c.vc, c.vs, c.pos, c.mass, rows, out)))
+
+
 def test_cache_class_refuses_what_cannot_work(cuda_dev):
     tc = TokenCache(1, 2, 2, 64, 64, n_sink=30, n_recent=30, device=cuda_dev)
     z = lambda T: torch.zeros(1, T, 2, 64, dtype=torch.bfloat16, device=cuda_dev)

@@ -208,6 +208,40 @@ def test_position_out_of_the_table_leaves_its_token_alone(cuda_dev):
         assert torch.equal(got, a.dwq)
 
 
+def test_what_does_not_fit_is_refused_and_odd_strides_of_one_element_are_not(cuda_dev):
+    B, T, Hq, Hkv, D = 1, 1, 2, 1, 64
+    cfg = P.make_qk_config(B, T, Hq, Hkv, D, torch.bfloat16, table_len=4)
+    f32 = dict(dtype=torch.float32, device=cuda_dev)
+    good = dict(q=torch.randn(B, T, Hq, D, device=cuda_dev).bfloat16(), k=torch.randn(B, T, Hkv, D, device=cuda_dev).bfloat16(),
+                q_weight=torch.rand(D, **f32), k_weight=torch.rand(D, **f32), cos=torch.rand(4, D // 2, **f32),
+                sin=torch.rand(4, D // 2, **f32), pos=torch.zeros(B, T, 1, dtype=torch.int32, device=cuda_dev),
+                q_out=torch.zeros(B, T, Hq, D, dtype=torch.bfloat16, device=cuda_dev),
+                k_out=torch.zeros(B, T, Hkv, D, dtype=torch.bfloat16, device=cuda_dev),
+                status=torch.zeros(1, dtype=torch.int32, device=cuda_dev))
+    order = list(good)
+    grads = lambda g: (g["q_out"], g["k_out"], torch.empty_like(good["q"]), torch.empty_like(good["k"]), None, None, None)
+    for name in order:
+        x = good[name]
+        bad = [x.cpu(), x.double(), x[None], x[..., :-1], None]
+        if name in ("q_out", "k_out"):
+            bad.append(x[..., :1, :].expand(B, T, 2, D) if name == "q_out" else x.transpose(-1, -2))
+        if name in ("q_weight", "k_weight"):
+            bad.pop()   # None: all ones
+        for y in bad:
+            g = dict(good, **{name: y})
+            with pytest.raises((P.PBSAError, AttributeError)):
+                P.pbsa_qk_norm_rope(cfg, *g.values())
+            if name not in ("q_out", "k_out"):
+                with pytest.raises((P.PBSAError, AttributeError)):
+                    P.pbsa_qk_norm_rope_bwd(cfg, *[g[n] for n in order[:7]], *grads(g), g["status"])
+    assert int(good["status"].item()) == 0 and not good["q_out"].any() and not good["k_out"].any()
+    P.pbsa_qk_norm_rope(cfg, *good.values())
+    odd = dict(good, q=good["q"].as_strided((1, 1, 2, 64), (3, 5, 64, 1)), k=good["k"].as_strided((1, 1, 1, 64), (1, 7, 9, 1)),
+               q_out=torch.zeros_like(good["q_out"]).as_strided((1, 1, 2, 64), (1, 1, 64, 1)), k_out=torch.zeros_like(good["k_out"]))
+    P.pbsa_qk_norm_rope(cfg, *odd.values())
+    assert torch.equal(odd["q_out"], good["q_out"]) and torch.equal(odd["k_out"], good["k_out"]) and good["q_out"].any()
+
+
 def test_no_tokens(cuda_dev):
     a = Heads(cuda_dev, T=0)
     a.fwd()
