@@ -255,3 +255,18 @@ def test_binding_refuses_tensors_that_do_not_fit():
         P.pbsa_qk_norm_rope(qc, *good[:7], k[:, :1].expand(2, 3, 2, 64), k, st)
     with pytest.raises(P.PBSAError):
         P.make_qk_config(2, 3, 2, 2, 64, axis_pairs=(8, 8, 8, 8))
+
+
+def test_quick_calls_leave_alone_what_is_not_on_the_device():
+    """The module behind the binding makes no call over CPU tensors, and none for no device."""
+    from block_sparse_attention_35_b200 import token_calls as C
+    cfg = P.make_qk_config(1, 1, 1, 1, 64, rot_dim=0)
+    x, st = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    args = (x, x, None, None, None, None, None, x, x, st)
+    for dev in (-1, 0):
+        assert C.qk_norm_rope(ctypes.addressof(cfg), dev, 0, *args) is None
+    assert C.qk_norm_rope(ctypes.addressof(cfg), 0, "stream", *args) is None
+    assert C.qk_norm_rope(ctypes.addressof(cfg), 0, 0, *([None] * 10)) is None
+    for f in (C.qk_norm_rope, C.qk_norm_rope_bwd, C.kv4_append, C.kv4_read, C.kv4_attn, C.kv4_evict):
+        with pytest.raises(TypeError):
+            f(ctypes.addressof(cfg), 0)
