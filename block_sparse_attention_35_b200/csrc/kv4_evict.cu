@@ -14,9 +14,10 @@
 // registers then count and write the rows in order: the counts of a warp need no barrier, and
 // one exchange between the warps and CTAs places them.  A single row (n = 1) is one reduction.
 //
-// L2 cold: 1 row of each of 32 x 8 caches of 8192 rows 7.7 us (16.8 MB, 2.2 TB/s; launch, one
-// round trip to memory and the reduction), 1560 rows of each of 12 caches of 18752 12.2 us (four
-// CTAs a cache: with one, which holds 19 keys a thread, 16.5 us).
+// L2 cold: 1 row of each of 32 x 8 caches of 8192 rows 5.7 us (16.8 MB, 2.9 TB/s; launch, one
+// round trip to memory and the reduction), all 256 CTAs at once: with 4-byte loads and one CTA an
+// SM 7.7.  1560 rows of each of 12 caches of 18752 9.7 us with eight CTAs a cache, 12.8 with four,
+// 16.5 with one, which holds 19 keys a thread.
 #include <cooperative_groups.h>
 
 #include "pbsa_device.cuh"
@@ -56,10 +57,10 @@ __device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* sums) {
     return v + before;
 }
 
-// K > 0: a thread keeps K keys; K = 0: `tiles` of them, read again in every round (a cache of
+// K > 0: a thread keeps K keys, a multiple of 4; K = 0: `tiles` of them, read again in every round (a cache of
 // more than kMaxCluster x 24576 rows).
 template <int K>
-__global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, K > 8 ? 1 : 2) evict_kernel(EvictArgs a, int tiles) {
     __shared__ unsigned hist[kBins];
     __shared__ unsigned sums[kWarps];
     __shared__ unsigned s_lt[kWarps], s_eq[kWarps];
@@ -74,36 +75,43 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a, int tiles)
     const int keep_from = a.keep_from ? a.keep_from[b] : 0x7fffffff;
     int32_t* rows = a.rows + (size_t)bh * a.n;
     const int per = K > 0 ? K : tiles;
-    const int row0 = (rank * kWarps + warp) * per * 32 + lane;   // this thread's rows: row0 + 32 j
+    // a warp's rows are consecutive, four in a row a thread: one 16-byte load for each array
+    const int row0 = (rank * kWarps + warp) * per * 32 + 4 * lane;
+    auto row = [&](int j) { return row0 + 128 * (j / 4) + j % 4; };
 
     uint32_t keys[K > 0 ? K : 1];
     if (K > 0) {
-        constexpr int kGroup = K > 8 ? 6 : K;   // loads in flight: twice as many
 #pragma unroll
-        for (int j0 = 0; j0 < K; j0 += kGroup) {
-            int p[kGroup > 0 ? kGroup : 1];
-            float m[kGroup > 0 ? kGroup : 1];
+        for (int j0 = 0; j0 < K; j0 += 8) {   // loads in flight: of eight keys
+            int4 p[2];
+            float4 m[2];
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                const int i = row0 + 32 * (j0 + j);
-                p[j] = i < a.N ? pos[i] : -1;
-                m[j] = i < a.N ? mass[i] : 0.f;
+            for (int v = 0; v < 2 && j0 + 4 * v < K; ++v) {
+                const int i = row(j0 + 4 * v);   // a multiple of 4, as N is
+                p[v] = i < a.N ? *reinterpret_cast<const int4*>(pos + i) : make_int4(-1, -1, -1, -1);
+                m[v] = i < a.N ? *reinterpret_cast<const float4*>(mass + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                keys[j0 + j] = row0 + 32 * (j0 + j) < a.N ? row_key(p[j], m[j], a.n_sink, keep_from) : kProtected;
+            for (int v = 0; v < 2 && j0 + 4 * v < K; ++v) {
+                const int j = j0 + 4 * v;
+                const bool in = row(j) < a.N;
+                keys[j] = in ? row_key(p[v].x, m[v].x, a.n_sink, keep_from) : kProtected;
+                keys[j + 1] = in ? row_key(p[v].y, m[v].y, a.n_sink, keep_from) : kProtected;
+                keys[j + 2] = in ? row_key(p[v].z, m[v].z, a.n_sink, keep_from) : kProtected;
+                keys[j + 3] = in ? row_key(p[v].w, m[v].w, a.n_sink, keep_from) : kProtected;
+            }
         }
     }
     auto key = [&](int j) -> uint32_t {
         if (K > 0) return keys[K > 0 ? j : 0];
-        const int i = row0 + 32 * j;
+        const int i = row(j);
         return i < a.N ? row_key(pos[i], mass[i], a.n_sink, keep_from) : kProtected;
     };
 
     if (a.n == 1) {   // the smallest (key, row) alone: no select
         unsigned long long best = ~0ull;
 #pragma unroll
-        for (int j = 0; j < per; ++j) best = min(best, ((unsigned long long)key(j) << 32) | (unsigned)(row0 + 32 * j));
+        for (int j = 0; j < per; ++j) best = min(best, ((unsigned long long)key(j) << 32) | (unsigned)row(j));
         const unsigned hi = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32));
         const unsigned lo = __reduce_min_sync(0xffffffffu, (unsigned)(best >> 32) == hi ? (unsigned)best : 0xffffffffu);
         if (ctas > 1) cluster.sync();   // the first CTA runs before its memory is written
@@ -135,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a, int tiles)
 #pragma unroll
         for (int j = 0; j < per; ++j) {
             const uint32_t k = key(j);
-            const bool in = (k & known) == prefix && row0 + 32 * j < a.N;
+            const bool in = (k & known) == prefix && row(j) < a.N;
             const unsigned who = __ballot_sync(0xffffffffu, in);
             if (who == 0) continue;
             const unsigned digit = (k >> shift) & mask;
@@ -206,13 +214,28 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs a, int tiles)
     unsigned eq_at = __reduce_add_sync(0xffffffffu, (lane < warp ? s_eq[lane] : 0u) + (lane < rank ? s_cta[lane][1] : 0u));
     const unsigned below = (1u << lane) - 1u;
 #pragma unroll
-    for (int j = 0; j < per; ++j) {
-        const uint32_t k = key(j);
-        const unsigned ml = __ballot_sync(0xffffffffu, k < tau), me = __ballot_sync(0xffffffffu, k == tau);
-        const unsigned l = lt_at + __popc(ml & below), e = eq_at + __popc(me & below);
-        if (k < tau || (k == tau && e < quota)) rows[l + min(e, quota)] = row0 + 32 * j;
-        lt_at += __popc(ml);
-        eq_at += __popc(me);
+    for (int j0 = 0; j0 < per; j0 += 4) {   // 128 consecutive rows
+        uint32_t k[4];
+        unsigned l = 0, e = 0, lts = 0, eqs = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            k[i] = key(j0 + i);
+            const unsigned ml = __ballot_sync(0xffffffffu, k[i] < tau), me = __ballot_sync(0xffffffffu, k[i] == tau);
+            l += __popc(ml & below);
+            e += __popc(me & below);
+            lts += __popc(ml);
+            eqs += __popc(me);
+        }
+        l += lt_at;
+        e += eq_at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (k[i] < tau || (k[i] == tau && e < quota)) rows[l + min(e, quota)] = row(j0 + i);
+            l += k[i] < tau;
+            e += k[i] == tau;
+        }
+        lt_at += lts;
+        eq_at += eqs;
     }
     if (tau == kProtected && rank == 0) {   // fewer than n rows may go
         unsigned all = __reduce_add_sync(0xffffffffu, lane < ctas ? s_cta[lane][0] : 0u);
@@ -240,16 +263,17 @@ cudaError_t run(const EvictArgs& a, int ctas, int tiles, cudaStream_t st) {
 
 cudaError_t launch_kv4_evict(const EvictArgs& a, cudaStream_t st) {
     const int tiles = (a.N + kThreads - 1) / kThreads;   // keys of a thread, with one CTA
-    if (tiles <= 2) return run<2>(a, 1, 0, st);
     auto cluster = [&](int keys) {
         int ctas = 1;
         while (keys * ctas < tiles) ctas *= 2;
         return ctas;
     };
-    // few heads: more CTAs for each, eight keys a thread
+    // few heads: more CTAs for each, four or eight keys a thread
+    if (tiles <= 4 * kMaxCluster && (tiles <= 4 || a.BH * cluster(4) <= kSMs)) return run<4>(a, cluster(4), 0, st);
     if (tiles <= 8 * kMaxCluster && (tiles <= 8 || a.BH * cluster(8) <= kSMs)) return run<8>(a, cluster(8), 0, st);
     if (tiles <= 24 * kMaxCluster) return run<24>(a, cluster(24), 0, st);
-    return run<0>(a, kMaxCluster, (tiles + kMaxCluster - 1) / kMaxCluster, st);
+    const int per = (tiles + kMaxCluster - 1) / kMaxCluster;
+    return run<0>(a, kMaxCluster, (per + 3) / 4 * 4, st);
 }
 
 }  // namespace pbsa
