@@ -9,14 +9,15 @@
 // as x times the scale's reciprocal, off by at most 2^-22 of it, and rounded to a multiple of
 // 2^-15 (by adding and subtracting 384): on a border, that gives the border again (a multiple
 // of 1/4), beside one it stays at least 2^-14 away.  The conversion then decides as exact
-// arithmetic would.  (A division a channel: 20.2 us for 4680 tokens of 12 heads, against 15.5.)  The same distances make one IEEE division exact enough for amax / 6 against
-// the borders of e4m3.
+// arithmetic would.  The same distances make one IEEE division exact enough for amax / 6 against
+// the borders of e4m3.  (4680 tokens of 12 heads: 20.2 us with a division a channel, 13.8 with the
+// largest magnitude and NaN found in fp32 and divisions for a thread's place, 11.8 so.)
 //
 // append_kernel and read_kernel are bound by HBM: one thread owns one block of sixteen
 // channels, 32 bytes of a 16-bit type against 8 bytes of codes and one scale byte; neighbouring
 // threads own neighbouring blocks, so a warp touches whole sectors on both sides.  4680 tokens
-// of 12 heads of 128 channels, L2 cold: append 13.7 us (28.8 MB read, 8.1 MB written, to
-// scattered rows), read 10.1 us; one token of 32 x 8 caches 2.9 and 2.6 us, launch and latency.
+// of 12 heads of 128 channels, L2 cold: append 11.8 us (28.8 MB read, 8.1 MB written, to
+// scattered rows), read 10.3 us; one token of 32 x 8 caches 2.9 and 2.6 us, launch and latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -45,21 +46,35 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b, __half*) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Quantises sixteen values (already divided by the unit): 8 bytes of codes and the scale byte.
-__device__ __forceinline__ uint2 quantise16(const float (&x)[16], uint8_t* scale) {
-    float amax = 0.f;
+__device__ constexpr uint32_t infinity_bits(__nv_bfloat16*) { return 0x7f80u; }
+__device__ constexpr uint32_t infinity_bits(__half*) { return 0x7c00u; }
+
+// The largest magnitude of sixteen values, as its bits: those order as the values do, and NaN
+// comes above infinity.
+__device__ __forceinline__ uint32_t top_bits(const uint32_t (&u)[8]) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, u[j] & 0x7fff7fffu);
+    return max(m & 0xffffu, m >> 16);
+}
+
+// Quantises sixteen values x `inv` (a power of two, one over the unit): 8 bytes of codes and the
+// scale byte.  `top`: the bits of the largest magnitude.  The unit goes into the scale's
+// reciprocal, which it leaves exact.
+template <typename T>
+__device__ __forceinline__ uint2 quantise16(const uint32_t (&u)[8], uint32_t top, float inv, uint8_t* scale) {
+    const float amax = widen2(top, static_cast<T*>(nullptr)).x * inv;
     const uint8_t sb = e4m3_from_float(__fdiv_rn(amax, 6.f));
     *scale = sb;
     const float s = e4m3_to_float(sb);
     uint32_t w[2] = {0, 0};
     if (s > 0.f) {
-        const float r = __frcp_rn(s);
+        const float r = __frcp_rn(s) * inv;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float lo = __fsub_rn(__fmaf_rn(x[2 * i], r, 384.f), 384.f);
-            const float hi = __fsub_rn(__fmaf_rn(x[2 * i + 1], r, 384.f), 384.f);
+            const float2 x = widen2(u[i], static_cast<T*>(nullptr));
+            const float lo = __fsub_rn(__fmaf_rn(x.x, r, 384.f), 384.f);
+            const float hi = __fsub_rn(__fmaf_rn(x.y, r, 384.f), 384.f);
             w[i / 4] |= e2m1x2_from_float(lo, hi) << (8 * (i % 4));
         }
     }
@@ -67,13 +82,13 @@ __device__ __forceinline__ uint2 quantise16(const float (&x)[16], uint8_t* scale
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(Kv4Args a, float inv_unit_k, float inv_unit_v) {
+__global__ void __launch_bounds__(kThreads, 8) append_kernel(Kv4Args a, float inv_unit_k, float inv_unit_v) {
     const pbsa_kv4_config& c = a.c;
-    const int gpr = c.D / 16;   // blocks of a row
+    const int log_gpr = c.D == 128 ? 3 : 2, gpr = 1 << log_gpr;   // blocks of a row
     // block -> (keys or values, sequence); thread -> (token, key head, block): the source's order
     const int is_v = blockIdx.z, b = blockIdx.y;
-    const unsigned i = blockIdx.x * kThreads + threadIdx.x, th = i / gpr;
-    const int g = i % gpr, t = th / c.Hkv, h = th - t * c.Hkv;
+    const unsigned i = blockIdx.x * kThreads + threadIdx.x, th = i >> log_gpr, Hkv = c.Hkv;
+    const int g = i & (gpr - 1), t = th / Hkv, h = th - t * Hkv;
     if (t >= a.T) return;
     // the source is on its way while the token's place is looked up
     const Strides& s = is_v ? a.sv : a.sk;
@@ -87,21 +102,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv4Args a, float inv_u
         set_status(a.status, PBSA_ERR_DEVICE_CHECK);
         return;
     }
-    const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    const float inv = is_v ? inv_unit_v : inv_unit_k;
-    float x[16];
-    bool nan = false;
+    uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    constexpr uint32_t kInf = infinity_bits(static_cast<T*>(nullptr));
+    uint32_t top = top_bits(u);
+    if (top > kInf) {   // a NaN becomes 0
+        set_status(a.status, PBSA_ERR_DEVICE_CHECK);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 v = widen2(u[j], static_cast<T*>(nullptr));
-        nan |= (v.x != v.x) || (v.y != v.y);
-        x[2 * j] = v.x == v.x ? v.x * inv : 0.f;
-        x[2 * j + 1] = v.y == v.y ? v.y * inv : 0.f;
+        for (int j = 0; j < 8; ++j)
+            u[j] &= ((u[j] & 0x7fffu) > kInf ? 0u : 0xffffu) | ((u[j] >> 16 & 0x7fffu) > kInf ? 0u : 0xffff0000u);
+        top = top_bits(u);
     }
-    if (nan) set_status(a.status, PBSA_ERR_DEVICE_CHECK);
-    const size_t at = (bh * c.capacity + row) * gpr + g;
+    const size_t at = ((bh * c.capacity + row) << log_gpr) + g;
     uint8_t scale;
-    const uint2 codes = quantise16(x, &scale);
+    const uint2 codes = quantise16<T>(u, top, is_v ? inv_unit_v : inv_unit_k, &scale);
     reinterpret_cast<uint2*>(is_v ? a.cache.v_codes : a.cache.k_codes)[at] = codes;
     (is_v ? a.cache.v_scales : a.cache.k_scales)[at] = scale;
     if (g == 0 && !is_v) {
@@ -113,11 +126,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv4Args a, float inv_u
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(Kv4Args a) {
     const pbsa_kv4_config& c = a.c;
-    const int gpr = c.D / 16;
+    const int log_gpr = c.D == 128 ? 3 : 2, gpr = 1 << log_gpr;
     // block -> (keys or values, sequence and key head); thread -> (row, block)
     const unsigned per = (unsigned)((a.n * gpr + kThreads - 1) / kThreads), bh = blockIdx.x / per;
     const unsigned i = (blockIdx.x - bh * per) * kThreads + threadIdx.x;
-    const int is_v = blockIdx.y, g = i % gpr, j = i / gpr;
+    const int is_v = blockIdx.y, g = i & (gpr - 1), j = i >> log_gpr;
     if (j >= a.n) return;
     const int row = a.rows ? a.rows[(size_t)bh * a.n + j] : j;
     uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
