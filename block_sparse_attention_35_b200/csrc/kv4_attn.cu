@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
 
         for (int blk = blk0; blk < blk1; ++blk) {
             const int row = blk * kBlock + warp * kUnit;
-            ok = ok && mbar_wait(&s_full[stage], phase, &s_abort, a.k.status);
+            ok = ok && mbar_wait_warp(&s_full[stage], phase, &s_abort, a.k.status);
             if (ok && row < len) {
                 const uint32_t at_stage = stage * (uint32_t)sizeof(Block<D>);
                 Keys<D> x;

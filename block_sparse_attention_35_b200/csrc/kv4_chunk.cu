@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
         bool ok = true;
         for (int t = 0; ok && t < tiles; ++t) {
             const int s = t & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_qfull[s], (t >> 1) & 1, &s_abort, a.k.status));
-            if (ok && t >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&s_free[s], ((t >> 1) - 1) & 1, &s_abort, a.k.status));
+            ok = mbar_wait_warp(&s_qfull[s], (t >> 1) & 1, &s_abort, a.k.status);
+            if (ok && t >= 2) ok = mbar_wait_warp(&s_free[s], ((t >> 1) - 1) & 1, &s_abort, a.k.status);
             if (!ok) break;
             tc_fence_after();
             const uint32_t q_lo = sdesc_lo(smem_u32(sQ + s * kTile), 16);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
             s_lim[group][buf][key] = __float_as_int(next.z);
             named_bar_sync(1 + group, 128);   // and the columns two tiles back have been read
             next = column(t + 2);
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status));
+            ok = ok && mbar_wait_warp(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status);
             if (ok) {
                 tc_fence_after();
                 uint64_t part[2][2] = {{0, 0}, {0, 0}};
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     const uint32_t tmem = s_tmem;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, &s_abort, a.k.status));
+        return mbar_wait_warp(bar, parity, &s_abort, a.k.status);
     };
 
     // A segment: what every role needs of it; and the step to the next one.

@@ -79,6 +79,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     }
 }
 
+// mbar_wait of a whole warp, with one verdict for all lanes: they look at the clock and the abort
+// flag one by one, so where one gives up another may still see the phase complete, and what
+// follows (shuffles, votes, matrix instructions of the full warp) needs all of them or none.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+                                               unsigned long long limit_ns = kWaitLimitNs) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, limit_ns));
+}
+
 // Same as mbar_wait but ignores the abort flag (used to drain in-flight copies).
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity,
                                                 unsigned long long limit_ns) {
