@@ -205,11 +205,6 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
             }
             __syncwarp();
         }
-        if (!ok) {   // the products already issued end before tensor memory is released
-            if (elect_one()) umma_commit(&s_drain);
-            __syncwarp();
-            mbar_wait_drain(&s_drain, 0, 100000000ull);
-        }
     } else {
         const int group = warp >> 2, key = tid & 127;
         const uint32_t addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * group;
@@ -313,6 +308,13 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {
+        // after a wait that gave up, in whichever warp: the products already issued end before
+        // tensor memory is released
+        if (s_abort) {
+            if (elect_one()) umma_commit(&s_drain);
+            __syncwarp();
+            mbar_wait_drain(&s_drain, 0, 100000000ull);
+        }
         tc_fence_after();
         tmem_dealloc(tmem, 256);
     }
@@ -502,11 +504,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     ++n_seg;
                 }
                 finish(s);
-            }
-            if (!ok) {   // the products already issued end before tensor memory is released
-                if (elect_one()) umma_commit(&s_drain[x]);
-                __syncwarp();
-                mbar_wait_drain(&s_drain[x], 0, 100000000ull);
             }
         } else {
             // -------------------------------------------------- the cache, into operands
@@ -707,6 +704,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
     }
     tc_fence_before();
     __syncthreads();
+    // after a wait that gave up, in whichever warp: the products already issued, by either of the
+    // two warps that issue, end before tensor memory is released
+    if (s_abort) {
+        if (warp >= 12) {
+            if (elect_one()) umma_commit(&s_drain[warp - 12]);
+            __syncwarp();
+            mbar_wait_drain(&s_drain[warp - 12], 0, 100000000ull);
+        }
+        __syncthreads();
+    }
     if (warp == 12) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
