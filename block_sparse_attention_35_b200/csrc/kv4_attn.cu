@@ -290,13 +290,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
                 uint32_t vmask[2] = {0xffffu, 0xffffu};   // of the scales of values 2c, 2c+1 and 2c+8, 2c+9
-                if (__any_sync(0xffffffffu, (x.pos[0] | x.pos[1]) < 0) || row + kUnit > len || choosy) {
+                const bool hide = __any_sync(0xffffffffu, (x.pos[0] | x.pos[1]) < 0) || row + kUnit > len || choosy;
+                if (hide) {
                     hide_keys(x, len - row, lane);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (x.pos[i >> 1] > lim(n, i & 1)) s[n][i] = -INFINITY;
                     // values of rows without a token: scale zero
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -305,6 +301,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                     }
                 }
                 scores<D, NT>(s, x, qf);
+                // over the products, not under them: those of a padded query may be NaN
+                if (hide) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (x.pos[i >> 1] > lim(n, i & 1)) s[n][i] = -INFINITY;
+                }
                 bool grow = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -545,11 +549,11 @@ __global__ void __launch_bounds__(kMassThreads) mass_logits_kernel(AttnArgs a) {
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-        if (r < a.R && lse[r] != -INFINITY) {   // a hidden row's logit is -inf: it adds 0
-            sum.x += ex2(v[r].x - lse[r]);
-            sum.y += ex2(v[r].y - lse[r]);
-            sum.z += ex2(v[r].z - lse[r]);
-            sum.w += ex2(v[r].w - lse[r]);
+        if (r < a.R && lse[r] != -INFINITY) {   // a hidden row's logit is -inf: it adds 0, whatever the lse
+            sum.x += v[r].x == -INFINITY ? 0.f : ex2(v[r].x - lse[r]);
+            sum.y += v[r].y == -INFINITY ? 0.f : ex2(v[r].y - lse[r]);
+            sum.z += v[r].z == -INFINITY ? 0.f : ex2(v[r].z - lse[r]);
+            sum.w += v[r].w == -INFINITY ? 0.f : ex2(v[r].w - lse[r]);
         }
     if (j < len && pos.x >= 0) mass.x += sum.x;
     if (j + 1 < len && pos.y >= 0) mass.y += sum.y;

@@ -587,9 +587,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                 tmem_ld32(s_at + 32, raw_s[1]);
                 const TileInfo& inf = info[(tile + u / 2) % kInfo];
                 const int newest = max(inf.newest[2 * j], inf.newest[2 * j + 1]);
-                // some row of this warp may not see some token of the step (rows past the last
-                // are never read back)
-                const bool causal = __any_sync(0xffffffffu, r < a.R && newest > lim);
+                // some row of this warp may not see some token of the step, or none has one (rows
+                // past the last are never read back).  Elsewhere every row sees a token, and
+                // adding -infinity to what a NaN query made of an empty row costs nothing more.
+                const bool causal = __any_sync(0xffffffffu, r < a.R && (newest > lim || newest < 0));
                 tmem_ld_wait();
                 float v[64];
 #pragma unroll

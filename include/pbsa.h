@@ -468,7 +468,9 @@ PBSA_API int pbsa_kv4_read(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cac
  *
  * Row j of (b, key head) is seen by query t when j < kv_len[b], pos[j] >= 0 and, with q_pos,
  * pos[j] <= q_pos[b][t].  A query that sees no row (an empty cache; q_pos -1, the padding of a
- * shorter sequence) gets out = 0 and lse = -infinity.
+ * shorter sequence) gets out = 0 and lse = -infinity and adds nothing to the masses, whatever it
+ * holds.  A NaN or an infinity in a query that sees rows makes its own output NaN, and the masses
+ * of the rows it sees.
  *
  *   q        [B, T, Hq, D]; strides NULL or 3 (batch, token, head)
  *   q_pos    nullable; [B, T] int32, the causal mask above
