@@ -55,14 +55,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// A power of two that brings a row's largest entry to [2^14, 2^15) in fp16 - exact but for
-// entries 2^-38 below it - and the factor that turns a product of the row so scaled into a
-// base-2 logit.
+// A power of two that brings a row's largest entry to [2^14, 2^15) in fp16 - entries keep an
+// absolute error of at most 2^-39 of it, half of fp16's smallest step (2^-145 where it is below
+// 2^-106 and not brought all the way); bf16 entries down to 2^-31 of it are exact - and the factor
+// that turns a product of the row so scaled into a base-2 logit.
+// The factor is at least the smallest normal number: where it would be less (a small unit, a tiny
+// row) every logit is next to zero anyway, and -infinity for a hidden key times zero would be NaN.
 __device__ __forceinline__ void query_scale(const AttnArgs& a, float amax, float& up, float& fac) {
     const int ex = (int)(__float_as_uint(amax) >> 23);   // biased; 255: inf
     const int e = (ex == 0 || ex == 255) ? 0 : min(14 - (ex - 127), 120);
     up = __uint_as_float((uint32_t)(127 + e) << 23);
-    fac = rsqrtf((float)a.k.c.D) * kLog2e * a.k.c.k_unit * __uint_as_float((uint32_t)(127 - e) << 23);
+    fac = fmaxf(rsqrtf((float)a.k.c.D) * kLog2e * a.k.c.k_unit * __uint_as_float((uint32_t)(127 - e) << 23),
+                __uint_as_float(1u << 23));
 }
 
 // Four channels from ch on of query row r, zeros past the last row.

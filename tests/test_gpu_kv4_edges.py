@@ -1,5 +1,5 @@
 """Edges of the 4-bit token cache's attention: queries that hold no number, against the same call on
-harmless inputs."""
+harmless inputs, and logits far below one, against the fp64 oracle."""
 import math
 
 import numpy as np
@@ -62,3 +62,20 @@ def test_a_query_without_a_number_leaves_the_masses_of_rows_it_does_not_see(cuda
     unseen = c.pos > N // 2
     assert torch.isfinite(mass[unseen]).all() and unseen.any()
     assert out[:, -1].isnan().all() and torch.isfinite(out[:, :-1]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,T", ROWS)
+@pytest.mark.parametrize("ku,size", [(2.0 ** -40, 2.0 ** -100), (2.0 ** -40, 2.0 ** -126), (2.0 ** -28, 2.0 ** -120),
+                                     (2.0 ** -40, 2.0 ** -60), (2.0 ** 40, 2.0 ** -126)])
+def test_tiny_queries_and_units_give_the_mean(cuda_dev, D, G, T, ku, size):
+    """Logits that are nearly zero: hidden and padded rows stay hidden, the others weigh alike."""
+    c = Cache(cuda_dev, B=2, Hq=G, Hkv=1, D=D, N=192, ku=ku, seed=5)
+    c.pos[torch.rand(c.pos.shape, generator=c.g).to(cuda_dev) < 0.2] = -1
+    q = (c.queries(T).float().clamp(-2, 2) * size).to(torch.bfloat16)
+    q_pos = torch.randint(0, 384, (2, T), generator=c.g, dtype=torch.int32).to(cuda_dev)
+    lens = [192, 70]
+    for pos in (None, q_pos):
+        mass = c.mass.clone()
+        out, lse = c.attend(q, pos, c.i32(lens), mass)
+        check_attention(c, q, pos, lens, out, lse, mass, c.mass)
