@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
     float* o_sm = reinterpret_cast<float*>(q_sm + kSteps * NT * 32);      // [kWarps][kRows][D]
     float* m_sm = o_sm + kWarps * kRows * D;                              // [kWarps][kRows]
     float* l_sm = m_sm + kWarps * kRows;                                  // [kWarps][kRows]
-    float* fac_sm = l_sm + kWarps * kRows;                                // [kRows]
+    float* join_fac = l_sm + kWarps * kRows;                              // [kRows]: the segment's, for its end
+    float* fac_sm = join_fac + kRows;                                     // [kRows]
     int* lim_sm = reinterpret_cast<int*>(fac_sm + kRows);                 // [kRows]
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, c = lane & 3;
     const int N = a.k.c.capacity;
@@ -229,7 +230,6 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                 if (a.q_frag && blk0 == 0 && r / 8 < a.tiles8) {
                     const size_t to = (size_t)bh * a.tiles8 + r / 8;
                     a.q_frag[(to * kSteps + j) * 32 + slot] = v;
-                    if (ch4 == 0) a.q_fac[to * 8 + (r & 7)] = f;
                 }
             }
         }
@@ -254,13 +254,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
         const bool choosy = a.k.q_pos || kRows > a.R;   // some row may not see some key
         float* lg = kLogits ? a.logits + ((size_t)bh * a.R + 2 * c) * N + g : nullptr;
 
-        float mref[NT][2], thr[NT][2], l[NT][2], o[NT][kSteps][4];
+        float ref[NT][2], thr[NT][2], l[NT][2], o[NT][kSteps][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mref[n][i] = -INFINITY;   // running maximum - kShift, common to the lanes of a row
-                thr[n][i] = -INFINITY;    // products above it raise the maximum: (maximum + kLag) / fac
+                ref[n][i] = 0.f;          // largest product (with the lag), common to the lanes of a row
+                thr[n][i] = -INFINITY;    // products above it raise it: ref + kLag / fac; -inf: none seen so far
                 l[n][i] = 0.f;            // this lane's share of the sum
             }
 #pragma unroll
@@ -323,41 +323,36 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                            const float mn = t * fac(n, i) - kShift;
-                            if (mn > mref[n][i]) {
-                                const float k = ex2(mref[n][i] - mn);   // 0 from the initial -inf
+                            const bool none = thr[n][i] == -INFINITY;
+                            if (t > (none ? -INFINITY : ref[n][i])) {
+                                const float k = none ? 0.f : ex2((ref[n][i] - t) * fac(n, i));
                                 l[n][i] *= k;
 #pragma unroll
                                 for (int j = 0; j < kSteps; ++j) {
                                     o[n][j][i] *= k;
                                     o[n][j][i + 2] *= k;
                                 }
-                                mref[n][i] = mn;
-                                thr[n][i] = (mn + kShift + kLag) / fac(n, i);
+                                ref[n][i] = t;
+                                thr[n][i] = __fadd_rd(t, kLag / fac(n, i));
                             }
                         }
                 }
                 uint32_t p[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float f[2], ref[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        f[i] = fac(n, i);
-                        ref[i] = mref[n][i] == -INFINITY ? 0.f : -mref[n][i];   // none seen so far: 2^-inf
-                    }
+                    const float f[2] = {fac(n, 0), fac(n, 1)};
                     if (kLogits) {   // NT == 1
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             if (2 * c + i < a.R) {
                                 float* dst = lg + (size_t)i * N + row;
-                                dst[0] = s[0][i] * f[i];
-                                dst[8] = s[0][i + 2] * f[i];
+                                dst[0] = s[0][i];
+                                dst[8] = s[0][i + 2];
                             }
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        s[n][i] = ex2(fmaf(s[n][i], f[i & 1], ref[i & 1]));
+                        s[n][i] = ex2(fmaf(s[n][i] - ref[n][i & 1], f[i & 1], kShift));
                         l[n][i & 1] += s[n][i];
                     }
 #pragma unroll
@@ -409,8 +404,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
                 const int r = 8 * n + 2 * c + i;
                 if (g == 0) {
-                    m_sm[warp * kRows + r] = mref[n][i];
+                    m_sm[warp * kRows + r] = thr[n][i] == -INFINITY ? -INFINITY : ref[n][i];
                     l_sm[warp * kRows + r] = t;
+                    if (warp == 0) join_fac[r] = fac(n, i);
                 }
                 float* dst = o_sm + ((size_t)warp * kRows + r) * D + g * (D / 8);
 #pragma unroll
@@ -426,21 +422,21 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
             float mx = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, m_sm[k * kRows + r]);
-            const float base = mx == -INFINITY ? 0.f : mx;
+            const float base = mx == -INFINITY ? 0.f : mx, fr = join_fac[r];
             float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                const float f = ex2(m_sm[k * kRows + r] - base);
+                const float f = ex2((m_sm[k * kRows + r] - base) * fr);
                 const float4 y = *reinterpret_cast<const float4*>(o_sm + ((size_t)k * kRows + r) * D + d);
                 t.x += f * y.x, t.y += f * y.y, t.z += f * y.z, t.w += f * y.w;
                 sum += f * l_sm[k * kRows + r];
             }
             if (whole) {
-                finish_row<D, T>(a, b, hkv, r, d, t, mx, sum);
+                finish_row<D, T>(a, b, hkv, r, d, t, mx, fr, sum);
             } else {
                 *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = t;
-                if (d == 0) a.part_ml[slot + r] = make_float2(mx, sum);
+                if (d == 0) a.part_ml[slot + r] = make_float4(mx, sum, fr, 0.f);
             }
         }
         if (n_use < total) {
@@ -487,16 +483,17 @@ __global__ void __launch_bounds__(kJoinThreads<D, PARTS>) join_kernel(AttnArgs a
     const bool split = valid && !(n > 0 && first == last);   // else written by its CTA, or no row
     // the first CTA's part is its last segment (slot 1), the others' their first (slot 0)
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float mx = -INFINITY, sum = 0.f;
+    float mx = -INFINITY, sum = 0.f, fac = 1.f;   // every part has the row's factor
     if (split && n > 0) {
         const size_t base = qrow % a.rows;
 #pragma unroll 4
         for (int i = first + part; i <= last; i += PARTS) {
             const size_t at = base + ((size_t)2 * i + (i == first)) * a.rows;
-            const float2 ml = a.part_ml[at];
+            const float4 ml = a.part_ml[at];
             const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + d);
             const float mn = fmaxf(mx, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(mx - ref), k = ex2(ml.x - ref);
+            fac = ml.z;
+            const float f = ex2((mx - ref) * fac), k = ex2((ml.x - ref) * fac);
             v.x = f * v.x + k * x.x, v.y = f * v.y + k * x.y, v.z = f * v.z + k * x.z, v.w = f * v.w + k * x.w;
             sum = f * sum + k * ml.y;
             mx = mn;
@@ -516,21 +513,21 @@ __global__ void __launch_bounds__(kJoinThreads<D, PARTS>) join_kernel(AttnArgs a
             sum = 0.f;
 #pragma unroll
             for (int i = 0; i < PARTS; ++i) {
-                const float k = ex2(s_m[mine][i] - ref);
+                const float k = ex2((s_m[mine][i] - ref) * fac);   // the first part's lanes have it
                 const float4 x = s_v[mine][i][threadIdx.x % kLanes];
                 v.x += k * x.x, v.y += k * x.y, v.z += k * x.z, v.w += k * x.w;
                 sum += k * s_l[mine][i];
             }
         }
     }
-    if (split && part == 0) finish_row<D, T>(a, b, hkv, qrow, d, v, mx, sum);
+    if (split && part == 0) finish_row<D, T>(a, b, hkv, qrow, d, v, mx, fac, sum);
 }
 
-// Masses from the kept logits of at most eight rows: a thread takes four cached rows.
+// Masses from the kept products of at most eight rows: a thread takes four cached rows.
 constexpr int kMassThreads = 128;
 
 __global__ void __launch_bounds__(kMassThreads) mass_logits_kernel(AttnArgs a) {
-    const int N = a.k.c.capacity, bh = blockIdx.x, b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv;
+    const int N = a.k.c.capacity, bh = blockIdx.x, b = bh / a.k.c.Hkv;
     const int j = (blockIdx.y * kMassThreads + threadIdx.x) * 4, len = used_rows(a, b);
     grid_dependency_wait();
     if (j >= len) return;
@@ -538,22 +535,22 @@ __global__ void __launch_bounds__(kMassThreads) mass_logits_kernel(AttnArgs a) {
     const size_t at = (size_t)bh * N + j;
     const int4 pos = *reinterpret_cast<const int4*>(a.k.cache.pos + at);
     float4 mass = *reinterpret_cast<const float4*>(a.k.mass + at);
-    float4 v[8];
-    float lse[8];
+    float4 v[8], ref[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r)
         if (r < a.R) {
             v[r] = *reinterpret_cast<const float4*>(s + (size_t)r * N);
-            lse[r] = a.k.lse[((size_t)b * a.k.c.Hq + hkv * a.G + r % a.G) * a.k.T + r / a.G] * kLog2e;
+            ref[r] = a.row_ref[(size_t)bh * a.R + r];
         }
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-        if (r < a.R && lse[r] != -INFINITY) {   // a hidden row's logit is -inf: it adds 0, whatever the lse
-            sum.x += v[r].x == -INFINITY ? 0.f : ex2(v[r].x - lse[r]);
-            sum.y += v[r].y == -INFINITY ? 0.f : ex2(v[r].y - lse[r]);
-            sum.z += v[r].z == -INFINITY ? 0.f : ex2(v[r].z - lse[r]);
-            sum.w += v[r].w == -INFINITY ? 0.f : ex2(v[r].w - lse[r]);
+        if (r < a.R) {   // a hidden row's product is -inf: it adds 0, whatever the reference
+            auto p = [&](float x) { return x == -INFINITY ? 0.f : ex2(fmaf(x - ref[r].x, ref[r].y, ref[r].z)); };
+            sum.x += p(v[r].x);
+            sum.y += p(v[r].y);
+            sum.z += p(v[r].z);
+            sum.w += p(v[r].w);
         }
     if (j < len && pos.x >= 0) mass.x += sum.x;
     if (j + 1 < len && pos.y >= 0) mass.y += sum.y;
@@ -563,16 +560,17 @@ __global__ void __launch_bounds__(kMassThreads) mass_logits_kernel(AttnArgs a) {
 }
 
 // Masses of up to 8 NT rows: the scores are formed again (half of the cache's bytes) once the
-// rows' lse is known; a warp owns its keys and takes all rows, so that every sum has one order
+// rows' sums are known; a warp owns its keys and takes all rows, so that every sum has one order
 // and one owner, and a code is turned into fp16 once.  Latency bounds it, so a warp of a large
 // call takes `run` units of keys with the next on its way (32 rows x 32 heads over 8192 cached
 // rows: 17.5 us, 22 with one unit a warp), and the first is read before the wait.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a, int run) {
     constexpr int kSteps = D / 16;
+    __shared__ float4 s_row[8 * NT];   // a row's reference, factor, exponent of the reference; its limit
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int N = a.k.c.capacity, units = N / kUnit, per_bh = (units + kMassWarps * run - 1) / (kMassWarps * run);
-    const int bh = blockIdx.x / per_bh, b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv;
+    const int bh = blockIdx.x / per_bh, b = bh / a.k.c.Hkv;
     const int len = used_rows(a, b), used = (len + kUnit - 1) / kUnit;
     int u = (blockIdx.x % per_bh) * kMassWarps * run + warp;
     const int end = min(used, u + kMassWarps * run);
@@ -584,19 +582,12 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a, int r
     Keys<D> x;   // the first is read while the kernels before still run
     if (u < end) load(x, u);
     grid_dependency_wait();
-    if (u >= end) return;
+    if (threadIdx.x < 8 * NT) {
+        const float4 rf = a.row_ref[(size_t)bh * a.R + min((int)threadIdx.x, a.R - 1)];
+        s_row[threadIdx.x] = make_float4(rf.x, rf.y, rf.z, __int_as_float(row_limit(a, b, threadIdx.x)));
+    }
+    __syncthreads();
     const uint2* q = a.q_frag + (size_t)bh * NT * kSteps * 32 + lane;
-    float fac[NT][2], lse[NT][2];
-    int lim[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 8 * n + 2 * c + i, rr = min(r, a.R - 1);
-            lim[n][i] = row_limit(a, b, r);
-            fac[n][i] = a.q_fac[((size_t)bh * NT + n) * 8 + 2 * c + i];
-            lse[n][i] = a.k.lse[((size_t)b * a.k.c.Hq + hkv * a.G + rr % a.G) * a.k.T + rr / a.G] * kLog2e;
-        }
     for (; u < end; u += kMassWarps) {
         const int unit = u;
         Keys<D> y = x;
@@ -612,10 +603,12 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a, int r
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+                const float4 rf = s_row[8 * n + 2 * c + i];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                    if (y.pos[k] <= lim[n][i]) sum[k] += ex2(s[n][i + 2 * k] * fac[n][i] - lse[n][i]);
+                    if (y.pos[k] <= __float_as_int(rf.w)) sum[k] += ex2(fmaf(s[n][i + 2 * k] - rf.x, rf.y, rf.z));
+            }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
@@ -651,7 +644,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace: parts of outputs and statistics, then what the masses and the many-row kernels need.
 struct Layout {
-    size_t part_o, part_ml, logits, q_frag, q_fac, q_tile, q_scale, bytes;
+    size_t part_o, part_ml, row_ref, logits, q_frag, q_tile, q_scale, bytes;
 
     Layout(const pbsa_kv4_config& c, int R) {
         AttnArgs a{};
@@ -664,8 +657,9 @@ struct Layout {
             return r;
         };
         part_o = take(slots * c.D * sizeof(float));
-        part_ml = take(slots * sizeof(float2));
-        logits = q_frag = q_fac = q_tile = q_scale = at;
+        part_ml = take(slots * sizeof(float4));
+        row_ref = take(bh * R * sizeof(float4));
+        logits = q_frag = q_tile = q_scale = at;
         if (chunk_takes(R)) {
             q_tile = take(bh * a.tiles128 * 128 * c.D * 2);
             q_scale = take(bh * a.tiles128 * 128 * sizeof(float));
@@ -673,7 +667,6 @@ struct Layout {
             logits = take(bh * c.capacity * R * sizeof(float));
         } else {
             q_frag = take(bh * a.tiles8 * (c.D / 16) * 32 * sizeof(uint2));
-            q_fac = take(bh * a.tiles8 * 8 * sizeof(float));
         }
         bytes = at;
     }
@@ -682,7 +675,7 @@ struct Layout {
 template <int D, int NT, typename T, bool kLogits>
 cudaError_t run_rows(const AttnArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(Block<D>) * kStages + (size_t)(D / 16) * NT * 32 * 8 +
-                        (size_t)kWarps * 8 * NT * (D + 2) * 4 + 8 * NT * 8;
+                        (size_t)kWarps * 8 * NT * (D + 2) * 4 + 8 * NT * 12;
     cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, NT, T, kLogits>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attn_kernel<D, NT, T, kLogits><<<(unsigned)a.ctas, 32 * (kWarps + 1), smem, st>>>(a);
@@ -743,7 +736,8 @@ cudaError_t launch_kv4_attn(const Kv4Args& k, cudaStream_t st) {
     const Layout lay(k.c, a.R);
     char* w = static_cast<char*>(k.workspace);
     a.part_o = reinterpret_cast<float*>(w + lay.part_o);
-    a.part_ml = reinterpret_cast<float2*>(w + lay.part_ml);
+    a.part_ml = reinterpret_cast<float4*>(w + lay.part_ml);
+    if (k.mass) a.row_ref = reinterpret_cast<float4*>(w + lay.row_ref);
     if (chunk_takes(a.R)) {
         a.q_tile = reinterpret_cast<uint8_t*>(w + lay.q_tile);
         a.q_scale = reinterpret_cast<float*>(w + lay.q_scale);
@@ -751,7 +745,6 @@ cudaError_t launch_kv4_attn(const Kv4Args& k, cudaStream_t st) {
         a.logits = reinterpret_cast<float*>(w + lay.logits);
     } else if (k.mass) {
         a.q_frag = reinterpret_cast<uint2*>(w + lay.q_frag);
-        a.q_fac = reinterpret_cast<float*>(w + lay.q_fac);
     }
     if (k.c.D == 64)
         return k.c.dtype == PBSA_DTYPE_BF16 ? run_attn<64, __nv_bfloat16>(a, st) : run_attn<64, __half>(a, st);

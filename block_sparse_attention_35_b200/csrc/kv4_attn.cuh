@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "kv4_device.cuh"
 #include "pbsa_device.cuh"
 #include "token_internal.cuh"
@@ -14,10 +16,17 @@ namespace pbsa {
 constexpr int kHidden = 0x7fffffff;        // position that no query sees
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Probabilities are kept as 2^(s - m + kShift) in fp16, m the running maximum or up to
-// kLag below it: at most 2^15, and what is lost below 2^-24 is under 2^-31 of the largest.
+// Probabilities are kept as 2^((s - m) fac + kShift) in fp16, s a product, fac its factor to a base-2
+// logit and m the largest product of the row so far or one at most kLag / fac below it: at most
+// 2^15, and what is lost below 2^-24 is under 2^-31 of the largest.  The difference is formed
+// before it is scaled: near the largest it is exact, while a logit of 2^24 and more, rounded
+// alone, would be off by whole powers of two, past fp16's range at 2^27.
 constexpr float kShift = 7.f;
 constexpr float kLag = 8.f;
+// Where a row's largest base-2 logit is below this, the difference may as well be formed by the
+// multiply-add that scales it: rounding the constant costs no more than 2^-24 of the logit, which
+// its product has lost already, and one instruction less for every score.
+constexpr float kNear = 256.f;
 
 // The T tokens x G query heads of one key head are the R = T G rows that share its keys; a CTA
 // takes `rows` of them at a time.
@@ -28,11 +37,11 @@ struct AttnArgs {
     int block;                 // keys of one piece of work
     int ctas;                  // CTAs that share the work
     float* part_o;             // [ctas][2][rows][D]
-    float2* part_ml;           // [ctas][2][rows]: base-2 maximum, sum
-    float* logits;             // [B Hkv][R][N] base-2 logits (mass of few rows)
+    float4* part_ml;           // [ctas][2][rows]: largest product, sum, factor of the row
+    float4* row_ref;           // [B Hkv][R] (masses): a probability is 2^((s - x) y + z)
+    float* logits;             // [B Hkv][R][N] products (mass of few rows)
     int tiles8;                // groups of 8 rows
     uint2* q_frag;             // [B Hkv][tiles8][D / 16][32] (mass of more rows)
-    float* q_fac;              // [B Hkv][tiles8][8]
     int tiles128;              // groups of 128 rows
     uint8_t* q_tile;           // [B Hkv][tiles128][128 rows x D fp16 as they lie in shared memory]
     float* q_scale;            // [B Hkv][tiles128][128]: factor from a product to a base-2 logit
@@ -61,12 +70,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // that turns a product of the row so scaled into a base-2 logit.
 // The factor is at least the smallest normal number: where it would be less (a small unit, a tiny
 // row) every logit is next to zero anyway, and -infinity for a hidden key times zero would be NaN.
+// It is at most the largest: where it would be more, so are logits, but not their differences' signs.
 __device__ __forceinline__ void query_scale(const AttnArgs& a, float amax, float& up, float& fac) {
     const int ex = (int)(__float_as_uint(amax) >> 23);   // biased; 255: inf
     const int e = (ex == 0 || ex == 255) ? 0 : min(14 - (ex - 127), 120);
     up = __uint_as_float((uint32_t)(127 + e) << 23);
-    fac = fmaxf(rsqrtf((float)a.k.c.D) * kLog2e * a.k.c.k_unit * __uint_as_float((uint32_t)(127 - e) << 23),
-                __uint_as_float(1u << 23));
+    fac = rsqrtf((float)a.k.c.D) * kLog2e * a.k.c.k_unit * __uint_as_float((uint32_t)(127 - e) << 23);
+    fac = fminf(fmaxf(fac, FLT_MIN), FLT_MAX);
 }
 
 // Four channels from ch on of query row r, zeros past the last row.
@@ -201,15 +211,25 @@ __device__ __forceinline__ void store4(T* p, const float4& v, float k) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(x);
 }
 
-// Four channels of a finished row: v = sum of probabilities times values, relative to 2^mx.
+// A finished row's lse and, where masses follow, its probabilities' reference.
+__device__ __forceinline__ void finish_sum(const AttnArgs& a, int b, int hkv, int row, int t, int h, float mx, float fac,
+                                           float sum) {
+    const float l2 = log2f(sum);
+    a.k.lse[((size_t)b * a.k.c.Hq + h) * a.k.T + t] = sum == 0.f ? -INFINITY : (fmaf(mx, fac, -kShift) + l2) * kLn2;
+    if (a.row_ref)   // a row that sees nothing: 2^-inf
+        a.row_ref[((size_t)b * a.k.c.Hkv + hkv) * a.R + row] =
+            sum == 0.f ? make_float4(0.f, 0.f, -INFINITY, 0.f) : make_float4(mx, fac, kShift - l2, 0.f);
+}
+
+// Four channels of a finished row: v = sum of probabilities times values, relative to the
+// product mx.
 template <int D, typename T>
 __device__ __forceinline__ void finish_row(const AttnArgs& a, int b, int hkv, int row, int d, const float4& v, float mx,
-                                           float sum) {
+                                           float fac, float sum) {
     const int t = row / a.G, h = hkv * a.G + row % a.G;
     store4(static_cast<T*>(a.k.out) + (((size_t)b * a.k.T + t) * a.k.c.Hq + h) * D + d, v,
            sum == 0.f ? 0.f : a.k.c.v_unit / sum);
-    if (d == 0)
-        a.k.lse[((size_t)b * a.k.c.Hq + h) * a.k.T + t] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    if (d == 0) finish_sum(a, b, hkv, row, t, h, mx, fac, sum);
 }
 
 // Launches a kernel that may start while the one before it in the stream still runs; every

@@ -9,7 +9,7 @@
 //                128 rows, ready for one bulk copy each.
 //  chunk_kernel  S = Q K^T, online softmax, O += P V for 256 rows a CTA (two sides of 128);
 //                CTAs split the work list as attn_kernel's do and join_kernel joins them.
-//  chunk_mass_kernel  S^T = K Q^T with the rows' final lse: a lane of tensor memory is a key, so
+//  chunk_mass_kernel  S^T = K Q^T with the rows' final sums: a lane of tensor memory is a key, so
 //                a key's mass is a sum along four threads' columns, with one owner and one order.
 #include "kv4_attn.cuh"
 
@@ -113,15 +113,17 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
     uint8_t* sK = sm;
     uint8_t* sQ = sm + kTile;   // [2][kTile]
     __shared__ __align__(8) uint64_t s_qfull[2], s_qfree[2], s_full[2], s_free[2], s_drain;
-    // by group of warps and tile: factors of two rows, their -lse; and limits
+    // by group of warps and tile, of two rows: factors, exponents of the products that they are
+    // relative to, and these with their sign turned; and limits
     __shared__ __align__(16) float s_col[2][2][64][4];
+    __shared__ __align__(8) float s_ref[2][2][128];
     __shared__ int s_lim[2][2][128];
     __shared__ float s_sum[128];
     __shared__ int s_pos[128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int N = a.k.c.capacity, per = (N + 127) / 128, bh = blockIdx.x / per, key0 = (blockIdx.x % per) * 128;
-    const int b = bh / a.k.c.Hkv, hkv = bh % a.k.c.Hkv, len = used_rows(a, b);
+    const int b = bh / a.k.c.Hkv, len = used_rows(a, b);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (key0 >= len) {
         grid_dependency_wait();
@@ -217,24 +219,21 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
             for (int i = 0; i < 2; ++i) pos[h][i] = s_pos[k0 + 16 * h + 8 * i];
         float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
         bool ok = true;
-        // a row's column: its factor, lse and limit; thread i prepares column i of the next tile
+        // a row's column: its reference and limit; thread i prepares column i of the next tile
         auto column = [&](int t) -> float4 {
             const int r = t * 128 + key;
-            float lse = INFINITY;
-            if (t < tiles && r < a.R) {
-                const int tt = r / a.G;
-                lse = a.k.lse[((size_t)b * a.k.c.Hq + hkv * a.G + r - tt * a.G) * a.k.T + tt] * kLog2e;
-                if (lse == -INFINITY) lse = INFINITY;   // a row that sees nothing adds nothing
-            }
-            return make_float4(t < tiles ? a.q_scale[(tile0 + t) * 128 + key] : 0.f, -lse,
-                               __int_as_float(row_limit(a, b, r)), 0.f);
+            float4 c = make_float4(0.f, 0.f, -INFINITY, 0.f);   // past the last row: 2^-inf
+            if (t < tiles && r < a.R) c = a.row_ref[(size_t)bh * a.R + r];
+            c.w = __int_as_float(row_limit(a, b, r));
+            return c;
         };
         float4 next = column(group);
         for (int t = group; t < tiles; t += 2) {
             const int buf = (t >> 1) & 1;
-            s_col[group][buf][key >> 1][key & 1] = next.x;
-            s_col[group][buf][key >> 1][2 + (key & 1)] = next.y;
-            s_lim[group][buf][key] = __float_as_int(next.z);
+            s_col[group][buf][key >> 1][key & 1] = next.y;
+            s_col[group][buf][key >> 1][2 + (key & 1)] = next.z;
+            s_ref[group][buf][key] = -next.x;
+            s_lim[group][buf][key] = __float_as_int(next.w);
             named_bar_sync(1 + group, 128);   // and the columns two tiles back have been read
             next = column(t + 2);
             ok = ok && mbar_wait_warp(&s_full[group], (t >> 1) & 1, &s_abort, a.k.status);
@@ -243,6 +242,7 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
                 uint64_t part[2][2] = {{0, 0}, {0, 0}};
                 uint32_t u[2][16];
                 float4 col[4];
+                uint64_t ref[4];
                 int2 lim[4];
                 tmem_ld_rows16(addr, u[0]);
 #pragma unroll
@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             col[j] = *reinterpret_cast<const float4*>(s_col[group][buf][c0 / 2 + 4 * j + c4]);
+                            ref[j] = *reinterpret_cast<const uint64_t*>(&s_ref[group][buf][c0 + 8 * j + 2 * c4]);
                             if (a.k.q_pos) lim[j] = *reinterpret_cast<const int2*>(&s_lim[group][buf][c0 + 8 * j + 2 * c4]);
                         }
                     }
@@ -266,8 +267,8 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float2 x = split(fma2(pair(__uint_as_float(u[k & 1][4 * j + 2 * i]), __uint_as_float(u[k & 1][4 * j + 2 * i + 1])),
-                                                  pair(col[j].x, col[j].y), pair(col[j].z, col[j].w)));
+                            const uint64_t s2 = pair(__uint_as_float(u[k & 1][4 * j + 2 * i]), __uint_as_float(u[k & 1][4 * j + 2 * i + 1]));
+                            float2 x = split(fma2(add2(s2, ref[j]), pair(col[j].x, col[j].y), pair(col[j].z, col[j].w)));
                             x.x = ex2(x.x), x.y = ex2(x.y);
                             if (a.k.q_pos) {
                                 x.x = pos[h][i] <= lim[j].x ? x.x : 0.f;
@@ -575,7 +576,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             const uint32_t o_at = tmem + lane_at + 256 + 128 * x;
             const float fac = a.q_scale[((size_t)s.bh * a.tiles128) * 128 + r];
             const int lim = row_limit(a, s.b, r);
-            float mref = -INFINITY, l = 0.f;
+            const float lag = kLag / fac;
+            float ref = 0.f, thr = -INFINITY, l = 0.f;   // ref, thr: as in attn_kernel
+            float c0 = kShift;                           // near rows: the exponent of a product of 0
+            bool far = false;                            // some row of the warp is not near (kNear)
             for (int u = 0; ok && u < 2 * s.tiles; ++u) {
                 const int j = u & 1;
                 ok = wait(&s_sfull[x][j], (n_mine + u / 2) & 1);
@@ -624,10 +628,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], e + 4 + k < 64 ? fmaxf(v[e + k], v[e + 4 + k]) : v[e + k]);
                 }
-                const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac - kShift;
-                const bool grow = mn > mref + kLag;
+                const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const bool grow = t > thr;
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float k = grow ? ex2(mref - mn) : 1.f;   // 0 from the initial -inf
+                    const float k = !grow ? 1.f : (thr == -INFINITY ? 0.f : ex2((ref - t) * fac));
                     if (u > 0) {
                         ok = wait(&s_pv[x][(u - 1) & 1], (n_mine + (u - 1) / 2) & 1);
                         if (!ok) break;
@@ -645,16 +649,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     }
                     if (grow) {
                         l *= k;
-                        mref = mn;
+                        ref = t;
+                        thr = __fadd_rd(t, lag);
+                    }
+                    far = __any_sync(0xffffffffu, fabsf(ref * fac) >= kNear);
+                    c0 = far ? kShift : fmaf(-ref, fac, kShift);
+                }
+                if (far) {
+                    const uint64_t m2 = pair(-ref, -ref);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 y = split(add2(pair(v[e], v[e + 1]), m2));
+                        v[e] = y.x, v[e + 1] = y.y;
                     }
                 }
-                const float ref = mref == -INFINITY ? 0.f : -mref;   // none seen so far: 2^-inf
-                const uint64_t fac2 = pair(fac, fac), ref2 = pair(ref, ref);
+                const uint64_t fac2 = pair(fac, fac), c2 = pair(c0, c0);
                 uint64_t part[2] = {0, 0};
                 uint32_t p[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    float2 y = split(fma2(pair(v[2 * e], v[2 * e + 1]), fac2, ref2));
+                    float2 y = split(fma2(pair(v[2 * e], v[2 * e + 1]), fac2, c2));
                     y.x = ex2(y.x), y.y = ex2(y.y);
                     part[e & 1] = add2(part[e & 1], pair(y.x, y.y));
                     const __half2 h = __floats2half2_rn(y.x, y.y);
@@ -692,10 +706,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
                     }
                 }
                 if (r < a.R) {
-                    if (whole)
-                        a.k.lse[((size_t)s.b * a.k.c.Hq + h) * a.k.T + tt] = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
-                    else
-                        a.part_ml[slot] = make_float2(mref, l);
+                    if (whole) finish_sum(a, s.b, s.hkv, r, tt, h, ref, fac, l);
+                    else a.part_ml[slot] = make_float4(thr == -INFINITY ? -INFINITY : ref, l, fac, 0.f);
                 }
             }
                 n_mine += s.tiles;
