@@ -378,6 +378,14 @@ def _want(t, name, shape, dtype, device, strided=False):
         _bad(f"{name} is not contiguous")
 
 
+def _want_heads(t, name, shape, dtype, device):
+    """Checks a [B, T, H, D] tensor as the library does too: strides and address multiples of 16 bytes."""
+    _want(t, name, shape, dtype, device, True)
+    if t.numel() and (t.data_ptr() % 16 or any(n > 1 and st * t.element_size() % 16
+                                               for n, st in zip(t.shape[:3], t.stride()))):
+        _bad(f"{name}: an address or a stride is not a multiple of 16 bytes")
+
+
 def _strides(*tensors):
     """Batch, token and head strides of [B, T, H, D] tensors (zeros for None, and where there is
     one element: its stride says nothing)."""

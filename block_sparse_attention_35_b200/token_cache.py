@@ -66,8 +66,11 @@ class TokenCache:
         """T new tokens of every sequence (n_new [B] int32 on the device: how many of them are
         tokens, the rest is padding; None: all) enter the cache and attend to it and to each
         other causally.  q [B, T, Hq, D], k, v [B, T, Hkv, D], normalised and rotated already.
-        Returns the output buffer [B, T, Hq, D] (zeros for padding)."""
+        Returns the output buffer [B, T, Hq, D] (zeros for padding).  What does not fit is refused
+        before anything changes."""
         T = q.shape[1]
+        for name, t, H in (("q", q, self.Hq), ("k", k, self.Hkv), ("v", v, self.Hkv)):
+            P._want_heads(t, name, (self.B, T, H, self.D), self.dtype, self.device)
         if T + self.n_sink + self.n_recent > self.capacity:
             raise ValueError(f"a step of {T} tokens does not fit beside {self.n_sink} sink and "
                              f"{self.n_recent} recent tokens in {self.capacity} rows")

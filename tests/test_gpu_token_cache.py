@@ -1,0 +1,43 @@
+"""TokenCache at its edges: refused and padded steps, many lengths, streams and graphs."""
+import pytest
+import torch
+
+from block_sparse_attention_35_b200 import pbsa as P
+from block_sparse_attention_35_b200.token_cache import TokenCache
+
+pytestmark = pytest.mark.gpu
+
+
+def tokens(dev, g, B, T, Hq, Hkv, D, dtype=torch.bfloat16):
+    return tuple(torch.randn(B, T, h, D, generator=g).to(dtype).to(dev) for h in (Hq, Hkv, Hkv))
+
+
+def state(tc):
+    return [t.clone() for t in (tc.k_codes, tc.k_scales, tc.v_codes, tc.v_scales, tc.pos, tc.mass, tc.seen,
+                                tc.kv_len, tc.status)]
+
+
+def test_a_refused_step_changes_nothing(cuda_dev):
+    """Every argument that does not fit, on a full cache whose rows are being given up."""
+    B, Hq, Hkv, D, N = 2, 4, 2, 64, 64
+    tc = TokenCache(B, Hq, Hkv, D, N, n_sink=2, n_recent=4, device=cuda_dev)
+    g = torch.Generator().manual_seed(0)
+    tc.step(*tokens(cuda_dev, g, B, 50, Hq, Hkv, D))
+    tc.step(*tokens(cuda_dev, g, B, 40, Hq, Hkv, D))
+    good = tokens(cuda_dev, g, B, 3, Hq, Hkv, D)
+    want = state(tc)
+    n_new = torch.tensor([3, 1], dtype=torch.int32, device=cuda_dev)
+    odd = lambda t: torch.zeros(t.numel() + 8, dtype=t.dtype, device=cuda_dev)[1:1 + t.numel()].view(t.shape)
+    wide = lambda t: torch.zeros(*t.shape[:3], D + 4, dtype=t.dtype, device=cuda_dev)[..., :D]
+    for i in range(3):
+        x = good[i]
+        for bad in (x.cpu(), x.half(), x.float(), x[:, :, :1], x[..., :32], x[:1], x[:, :2] if i else x[None],
+                    x.transpose(2, 3).contiguous().transpose(2, 3), odd(x), wide(x)):
+            args = list(good)
+            args[i] = bad
+            for n in (None, n_new):
+                with pytest.raises((P.PBSAError, ValueError)):
+                    tc.step(*args, n)
+    assert all(torch.equal(a, b) for a, b in zip(state(tc), want))
+    tc.step(*good, n_new)
+    assert tc.seen.tolist() == [93, 91] and int(tc.status.item()) == 0
