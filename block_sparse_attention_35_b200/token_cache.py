@@ -64,13 +64,16 @@ class TokenCache:
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_new=None):
         """T new tokens of every sequence (n_new [B] int32 on the device: how many of them are
-        tokens, the rest is padding; None: all) enter the cache and attend to it and to each
-        other causally.  q [B, T, Hq, D], k, v [B, T, Hkv, D], normalised and rotated already.
+        tokens, from 0 to T, beyond which it counts as the nearer of the two; the rest is padding;
+        None: all) enter the cache and attend to it and to each other causally.  q [B, T, Hq, D], k, v [B, T, Hkv, D], normalised and rotated already.
         Returns the output buffer [B, T, Hq, D] (zeros for padding).  What does not fit is refused
         before anything changes."""
         T = q.shape[1]
         for name, t, H in (("q", q, self.Hq), ("k", k, self.Hkv), ("v", v, self.Hkv)):
             P._want_heads(t, name, (self.B, T, H, self.D), self.dtype, self.device)
+        if n_new is not None and (n_new.shape != (self.B,) or n_new.dtype not in (torch.int32, torch.int64)
+                                  or n_new.device != self.device):
+            raise ValueError(f"n_new is not a tensor of {self.B} int32 on {self.device}")
         if T + self.n_sink + self.n_recent > self.capacity:
             raise ValueError(f"a step of {T} tokens does not fit beside {self.n_sink} sink and "
                              f"{self.n_recent} recent tokens in {self.capacity} rows")
@@ -78,8 +81,8 @@ class TokenCache:
         pos = self.seen[:, None] + s["ar"]
         n = T
         if n_new is not None:
-            n = n_new
-            pos = torch.where(s["ar"] < n_new[:, None], pos, torch.full_like(pos, -1))
+            n = n_new.clamp(0, T).int()
+            pos = torch.where(s["ar"] < n[:, None], pos, torch.full_like(pos, -1))
         P.pbsa_kv4_evict(self.cfg, self.pos, self.mass, self.n_sink, self.seen - self.n_recent,
                          s["rows"], self.status)
         P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, s["rows"], self.mass, self.status)

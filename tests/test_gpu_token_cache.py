@@ -41,3 +41,26 @@ def test_a_refused_step_changes_nothing(cuda_dev):
     assert all(torch.equal(a, b) for a, b in zip(state(tc), want))
     tc.step(*good, n_new)
     assert tc.seen.tolist() == [93, 91] and int(tc.status.item()) == 0
+
+
+def test_counts_beyond_the_step_are_held_to_it(cuda_dev):
+    """n_new below 0 counts as 0 and above T as T: positions never repeat and never skip."""
+    B, Hq, Hkv, D, N = 3, 2, 1, 64, 64
+    a, b = (TokenCache(B, Hq, Hkv, D, N, n_sink=2, n_recent=4, device=cuda_dev) for _ in range(2))
+    g = torch.Generator().manual_seed(1)
+    for given, meant in (([9, -3, 2], [3, 0, 2]), ([2 ** 31 - 1, -2 ** 31, 1], [3, 0, 1]), ([3, 3, 0], [3, 3, 0])):
+        x = tokens(cuda_dev, g, B, 3, Hq, Hkv, D)
+        i = lambda v, dt=torch.int32: torch.tensor(v, dtype=dt, device=cuda_dev)
+        oa, ob = a.step(*x, i(given)), b.step(*x, i(meant, torch.int64))
+        assert torch.equal(oa, ob) and all(torch.equal(u, v) for u, v in zip(state(a), state(b)))
+    assert a.seen.tolist() == [9, 3, 3] and a.kv_len.tolist() == [9, 3, 3] and int(a.status.item()) == 0
+
+
+def test_counts_of_another_kind_are_refused(cuda_dev):
+    tc = TokenCache(2, 2, 1, 64, 64, n_sink=2, n_recent=4, device=cuda_dev)
+    x = tokens(cuda_dev, torch.Generator().manual_seed(2), 2, 3, 2, 1, 64)
+    n = torch.tensor([1, 2], dtype=torch.int32, device=cuda_dev)
+    for bad in (n.cpu(), n[:1], n[:, None], n.float(), n.bool()):
+        with pytest.raises(ValueError):
+            tc.step(*x, bad)
+    assert (tc.pos == -1).all() and tc.seen.tolist() == [0, 0]
