@@ -8,10 +8,10 @@ object owns the device tensors; every step of the method runs in the kernels beh
     cache = TokenCache(B, Hq, Hkv, D, capacity=4096, n_sink=4, n_recent=256)
     out = cache.step(q, k, v)        # rows for the new tokens, append, causal attention
 
-Until the cache is full the new tokens take empty rows; then they take the rows that drew the
-least attention so far, sparing the sequence's first ``n_sink`` and its last ``n_recent`` tokens.
-(A padded sequence of the step that fills the cache may give up a row while an empty one is left:
-the chosen rows are taken in row order.)
+Until the cache is full the new tokens take empty rows; then a step of T tokens takes the T rows
+that drew the least attention so far, sparing the sequence's first ``n_sink`` and its last
+``n_recent`` tokens.  A padded sequence, with fewer tokens than T, takes what is empty first and
+then the first of those T rows in the order of the cache, not the lightest of them.
 Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph (run one
 before, so that its buffers exist)."""
 from __future__ import annotations
@@ -85,7 +85,11 @@ class TokenCache:
             pos = torch.where(s["ar"] < n[:, None], pos, torch.full_like(pos, -1))
         P.pbsa_kv4_evict(self.cfg, self.pos, self.mass, self.n_sink, self.seen - self.n_recent,
                          s["rows"], self.status)
-        P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, s["rows"], self.mass, self.status)
+        rows = s["rows"]
+        if n_new is not None:   # empty rows first: the last of them may stand behind rows in use
+            used = self.pos.gather(2, rows.clamp(min=0).long()) >= 0
+            rows = rows.gather(2, used.int().argsort(dim=-1, stable=True))
+        P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, rows, self.mass, self.status)
         self.seen += n
         self.kv_len += n
         self.kv_len.clamp_(max=self.capacity)

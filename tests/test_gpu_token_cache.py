@@ -64,3 +64,24 @@ def test_counts_of_another_kind_are_refused(cuda_dev):
         with pytest.raises(ValueError):
             tc.step(*x, bad)
     assert (tc.pos == -1).all() and tc.seen.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("n", [[2, 1], [1, 0], [0, 2], [3, 3]])
+def test_padded_steps_take_empty_rows_before_rows_in_use(cuda_dev, n):
+    """Two rows are empty, a step of three asks for one more: a sequence that has no more than two
+    tokens in it gives up nothing."""
+    B, Hq, Hkv, D, N = 2, 4, 2, 64, 64
+    tc = TokenCache(B, Hq, Hkv, D, N, n_sink=2, n_recent=4, device=cuda_dev)
+    g = torch.Generator().manual_seed(3)
+    tc.step(*tokens(cuda_dev, g, B, 40, Hq, Hkv, D))
+    tc.step(*tokens(cuda_dev, g, B, 22, Hq, Hkv, D))
+    assert (tc.pos[:, :, :62] >= 0).all() and (tc.pos[:, :, 62:] == -1).all()
+    before = tc.pos.clone()
+    tc.step(*tokens(cuda_dev, g, B, 3, Hq, Hkv, D), torch.tensor(n, dtype=torch.int32, device=cuda_dev))
+    for b, m in enumerate(n):
+        kept = (tc.pos[b] == before[b])[:, :62].sum(-1)
+        assert kept.tolist() == [62 - max(0, m - 2)] * Hkv
+        held = tc.pos[b].sort(-1).values[:, N - min(m, 3):] if m else tc.pos[b][:, :0]
+        assert held.tolist() == [list(range(62, 62 + m))] * Hkv
+        assert (tc.pos[b] == -1).sum(-1).tolist() == [max(0, 2 - m)] * Hkv
+    assert tc.kv_len.tolist() == [min(N, 62 + m) for m in n] and int(tc.status.item()) == 0
