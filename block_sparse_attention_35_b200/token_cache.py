@@ -13,12 +13,17 @@ that drew the least attention so far, sparing the sequence's first ``n_sink`` an
 ``n_recent`` tokens.  A padded sequence, with fewer tokens than T, takes what is empty first and
 then the first of those T rows in the order of the cache, not the lightest of them.
 Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph (run one
-before, so that its buffers exist)."""
+before, so that its buffers exist).  A step's output is a buffer that the next step of the same T
+writes again.  The buffers of the last ``_KEEP`` lengths are kept for the next step of their
+length, and those of a captured step as long as the cache."""
 from __future__ import annotations
 
 import torch
 
 from . import pbsa as P
+
+
+_KEEP = 4
 
 
 class TokenCache:
@@ -47,27 +52,40 @@ class TokenCache:
         self.seen = torch.zeros(B, **i32)       # tokens of every sequence so far
         self.kv_len = torch.zeros(B, **i32)     # rows in use
         self.status = torch.zeros(1, **i32)
-        self._steps = {}
+        self._steps = {}                        # by T: see _buffers
 
     def _buffers(self, T: int):
-        """The tensors of a step of T tokens, allocated on its first use."""
-        if T not in self._steps:
+        """The tensors of a step of T tokens, allocated on its first use; the least recently used
+        ones are given up, but for those whose addresses a graph holds."""
+        s = self._steps.pop(T, None)
+        capturing = torch.cuda.is_current_stream_capturing()
+        if s is None:
+            if not capturing:
+                spare = [n for n, x in self._steps.items() if not x["captured"]]
+                for n in spare[:max(0, len(spare) + 1 - _KEEP)]:
+                    for t in self._steps.pop(n).values():
+                        if torch.is_tensor(t):   # this stream may still work on it
+                            t.record_stream(torch.cuda.current_stream(self.device))
             dev = self.device
-            self._steps[T] = dict(
+            s = dict(
+                captured=False,
                 ar=torch.arange(T, dtype=torch.int32, device=dev),
                 rows=torch.empty(self.B, self.Hkv, T, dtype=torch.int32, device=dev),
                 out=torch.empty(self.B, T, self.Hq, self.D, dtype=self.dtype, device=dev),
                 lse=torch.empty(self.B, self.Hq, T, dtype=torch.float32, device=dev),
                 ws=torch.empty(P.pbsa_kv4_workspace_size(self.cfg, T), dtype=torch.uint8,
                                device=dev))
-        return self._steps[T]
+        s["captured"] |= capturing
+        self._steps[T] = s   # the last: in order of use
+        return s
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_new=None):
         """T new tokens of every sequence (n_new [B] int32 on the device: how many of them are
         tokens, from 0 to T, beyond which it counts as the nearer of the two; the rest is padding;
-        None: all) enter the cache and attend to it and to each other causally.  q [B, T, Hq, D], k, v [B, T, Hkv, D], normalised and rotated already.
-        Returns the output buffer [B, T, Hq, D] (zeros for padding).  What does not fit is refused
-        before anything changes."""
+        None: all) enter the cache and attend to it and to each other causally.  q [B, T, Hq, D],
+        k, v [B, T, Hkv, D], normalised and rotated already.  Returns the output [B, T, Hq, D]
+        (zeros for padding), which the next step of T tokens writes again.  What does not fit is
+        refused before anything changes."""
         T = q.shape[1]
         for name, t, H in (("q", q, self.Hq), ("k", k, self.Hkv), ("v", v, self.Hkv)):
             P._want_heads(t, name, (self.B, T, H, self.D), self.dtype, self.device)

@@ -85,3 +85,39 @@ def test_padded_steps_take_empty_rows_before_rows_in_use(cuda_dev, n):
         assert held.tolist() == [list(range(62, 62 + m))] * Hkv
         assert (tc.pos[b] == -1).sum(-1).tolist() == [max(0, 2 - m)] * Hkv
     assert tc.kv_len.tolist() == [min(N, 62 + m) for m in n] and int(tc.status.item()) == 0
+
+
+def test_buffers_of_many_lengths_do_not_pile_up(cuda_dev):
+    """Steps of thirty lengths hold the buffers of a few; a captured step keeps its own, and its
+    replay between them gives what an eager step gives."""
+    B, Hq, Hkv, D, N = 1, 8, 2, 64, 1024
+    a, b = (TokenCache(B, Hq, Hkv, D, N, n_sink=2, n_recent=8, device=cuda_dev) for _ in range(2))
+    g = torch.Generator().manual_seed(4)
+    static = [torch.zeros_like(t) for t in tokens(cuda_dev, g, B, 2, Hq, Hkv, D)]
+    for tc in (a, b):
+        tc.step(*static)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = a.step(*static)
+    sizes, held, outs = [], [torch.cuda.memory_allocated()], []
+    for T in [*range(60, 90), 3]:
+        x = tokens(cuda_dev, g, B, T, Hq, Hkv, D)
+        oa, ob = a.step(*x), b.step(*x)
+        assert torch.equal(oa, ob)
+        outs.append((oa, oa.clone()))
+        del outs[:-3]
+        assert all(torch.equal(x, y) for x, y in outs)     # nothing writes to an output of another length
+        for s, t in zip(static, tokens(cuda_dev, g, B, 2, Hq, Hkv, D)):
+            s.copy_(t)
+        graph.replay()
+        assert torch.equal(replayed, b.step(*static))
+        sizes.append(len(a._steps))
+        held.append(torch.cuda.memory_allocated())
+    assert all(torch.equal(x, y) for x, y in zip(state(a), state(b)))
+    assert max(sizes) <= 5 and 2 in a._steps
+    # Each of the two caches keeps four lengths and makes a fifth; outs holds six outputs and a
+    # step's inputs and comparisons are smaller than a length's buffers.  Buffers grow with T (from
+    # 65 tokens on, 260 query rows a head are two groups and the parts' count doubles), so the
+    # largest length bounds them all: 2 (4 + 1) + 1 of it, of thirty.
+    most = P.pbsa_kv4_workspace_size(a.cfg, 89) + 89 * Hq * (D * 2 + 4) + 89 * (Hkv + 1) * 4 + 5 * 512
+    assert max(held) - held[0] <= 11 * most
