@@ -12,8 +12,7 @@ Until the cache is full the new tokens take empty rows; then a step of T tokens 
 that drew the least attention so far, sparing the sequence's first ``n_sink`` and its last
 ``n_recent`` tokens.  A padded sequence, with fewer tokens than T, takes what is empty first and
 then the first of those T rows in the order of the cache, not the lightest of them.
-Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph (run one
-before, so that its buffers exist).  A step's output is a buffer that the next step of the same T
+Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph.  A step's output is a buffer that the next step of the same T
 writes again.  The buffers of the last ``_KEEP`` lengths are kept for the next step of their
 length, and those of a captured step as long as the cache."""
 from __future__ import annotations
@@ -52,6 +51,7 @@ class TokenCache:
         self.seen = torch.zeros(B, **i32)       # tokens of every sequence so far
         self.kv_len = torch.zeros(B, **i32)     # rows in use
         self.status = torch.zeros(1, **i32)
+        self._count = torch.arange(capacity, **i32)
         self._steps = {}                        # by T: see _buffers
 
     def _buffers(self, T: int):
@@ -69,7 +69,7 @@ class TokenCache:
             dev = self.device
             s = dict(
                 captured=False,
-                ar=torch.arange(T, dtype=torch.int32, device=dev),
+                ar=self._count[:T],
                 rows=torch.empty(self.B, self.Hkv, T, dtype=torch.int32, device=dev),
                 out=torch.empty(self.B, T, self.Hq, self.D, dtype=self.dtype, device=dev),
                 lse=torch.empty(self.B, self.Hq, T, dtype=torch.float32, device=dev),

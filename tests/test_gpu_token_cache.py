@@ -121,3 +121,26 @@ def test_buffers_of_many_lengths_do_not_pile_up(cuda_dev):
     # largest length bounds them all: 2 (4 + 1) + 1 of it, of thirty.
     most = P.pbsa_kv4_workspace_size(a.cfg, 89) + 89 * Hq * (D * 2 + 4) + 89 * (Hkv + 1) * 4 + 5 * 512
     assert max(held) - held[0] <= 11 * most
+
+
+@pytest.mark.parametrize("replay", [False, True])
+def test_a_length_that_was_captured_first(cuda_dev, replay):
+    """Buffers that a capture allocated serve eager steps too, before any replay and after."""
+    B, Hq, Hkv, D, N = 2, 4, 2, 64, 64
+    a, b = (TokenCache(B, Hq, Hkv, D, N, n_sink=2, n_recent=4, device=cuda_dev) for _ in range(2))
+    g = torch.Generator().manual_seed(5)
+    x = tokens(cuda_dev, g, B, 1, Hq, Hkv, D)
+    a.step(*x), b.step(*x)
+    n = torch.tensor([3, 2], dtype=torch.int32, device=cuda_dev)
+    x = tokens(cuda_dev, g, B, 3, Hq, Hkv, D)
+    torch.full((64,), -7, dtype=torch.int32, device=cuda_dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = a.step(*x, n)
+    if replay:
+        graph.replay()
+        assert torch.equal(out, b.step(*x, n))
+    for _ in range(2):
+        y = tokens(cuda_dev, g, B, 3, Hq, Hkv, D)
+        assert torch.equal(a.step(*y, n), b.step(*y, n))
+    assert all(torch.equal(u, v) for u, v in zip(state(a), state(b)))
