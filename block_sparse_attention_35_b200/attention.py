@@ -95,8 +95,12 @@ class SparseForcingAttention:
         self.ws_fwd = torch.empty(max(1, P.pbsa_workspace_size(self.cfg, P.PBSA_OP_FWD, qf)), **u8)
         self.ws_bwd = torch.empty(max(1, P.pbsa_workspace_size(self.cfg, P.PBSA_OP_BWD, qf)), **u8)
         self._grads = None
-        self._heads = {}              # by frames of the call: see norm_rope
-        self._rope = None
+        # norm_rope: a head's pairs turn by frame, row and column; every token's position
+        p, frames = D // 2, max(max_seq_len // self.tf, frame_h, frame_w)
+        self._pairs = (p - 2 * (p // 3), p // 3, p // 3)
+        self._rope = rope_table(self._pairs, frames, device=dev)
+        t = torch.arange(frames * self.tf, device=dev)
+        self._pos = torch.stack((t // self.tf, t % self.tf // frame_w, t % frame_w), -1).int()
 
     # ------------------------------------------------------------------ cache plumbing
     def ring_slot(self, p: int) -> int:
@@ -147,31 +151,13 @@ class SparseForcingAttention:
             self.pers_src.copy_(pers_src)
 
     # ------------------------------------------------------- heads: norm and rotation
-    def _heads_of(self, n_frames: int, grad_dtype):
-        """Configuration and position buffer of norm_rope calls over n_frames frames."""
-        key = (n_frames, grad_dtype)
-        if key not in self._heads:
-            p = self.D // 2
-            pairs = (p - 2 * (p // 3), p // 3, p // 3)     # frame, row, column
-            fh, fw = self.cfg.frame_h, self.cfg.frame_w
-            length = max(self.cfg.max_seq_len // self.tf, fh, fw)
-            if self._rope is None:
-                self._rope = rope_table(pairs, length, device=self.device)
-            cfg = P.make_qk_config(self.B, n_frames * self.tf, self.H, self.H, self.D,
-                                   interleaved=True, axis_pairs=pairs, table_len=length,
-                                   grad_dtype=grad_dtype)
-            t = torch.arange(n_frames * self.tf, device=self.device)
-            pos = torch.stack((t // self.tf, t % self.tf // fw, t % fw), -1).int()
-            pos = pos.expand(self.B, -1, -1).contiguous()
-            ws = torch.empty(P.pbsa_qk_workspace_size(cfg), dtype=torch.uint8, device=self.device)
-            self._heads[key] = cfg, pos, ws
-        return self._heads[key]
-
-    def _head_positions(self, pos, first_frame: int):
-        if first_frame:
-            pos = pos.clone()
-            pos[..., 0] += first_frame
-        return pos
+    def _heads_of(self, tokens: int, first_frame: int, grad_dtype):
+        """Configuration and positions [B, tokens, 3] of a norm_rope call."""
+        cfg = P.make_qk_config(self.B, tokens, self.H, self.H, self.D, interleaved=True,
+                               axis_pairs=self._pairs, table_len=self._rope[0].shape[0],
+                               grad_dtype=grad_dtype)
+        at = first_frame * self.tf
+        return cfg, self._pos[at:at + tokens].expand(self.B, -1, -1).contiguous()
 
     def norm_rope(self, q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, first_frame: int):
         """RMS-normalises every head of the projected queries and keys [B, frames*T_f, H, D]
@@ -179,23 +165,23 @@ class SparseForcingAttention:
         and rotates it by its token's frame (first_frame, first_frame + 1, ... of the sequence,
         below max_seq_len / T_f), row and column.  Returns new (q, k), ready for append() and
         the call."""
-        cfg, pos, _ = self._heads_of(q.shape[1] // self.tf, torch.bfloat16)
+        cfg, pos = self._heads_of(q.shape[1], first_frame, torch.bfloat16)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        P.pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, *self._rope,
-                            self._head_positions(pos, first_frame), q_out, k_out, self.status)
+        P.pbsa_qk_norm_rope(cfg, q, k, q_weight, k_weight, *self._rope, pos, q_out, k_out,
+                            self.status)
         return q_out, k_out
 
     def norm_rope_backward(self, q, k, q_weight, k_weight, first_frame: int, dq_out, dk_out):
         """Gradients of norm_rope from those of its outputs (bf16, or fp32 as backward() gives
         them).  Returns (dq, dk, dq_weight, dk_weight); a weight that is None has no gradient."""
-        cfg, pos, ws = self._heads_of(q.shape[1] // self.tf, dq_out.dtype)
+        cfg, pos = self._heads_of(q.shape[1], first_frame, dq_out.dtype)
         dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
         dw = [None if w is None else torch.empty_like(w) for w in (q_weight, k_weight)]
-        P.pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, *self._rope,
-                                self._head_positions(pos, first_frame), dq_out, dk_out, dq, dk,
-                                dw[0], dw[1], ws, self.status)
+        ws = torch.empty(P.pbsa_qk_workspace_size(cfg), dtype=torch.uint8, device=self.device)
+        P.pbsa_qk_norm_rope_bwd(cfg, q, k, q_weight, k_weight, *self._rope, pos, dq_out, dk_out,
+                                dq, dk, dw[0], dw[1], ws, self.status)
         return dq, dk, dw[0], dw[1]
 
     # ------------------------------------------------------------------ the method
