@@ -157,6 +157,8 @@ class SparseForcingAttention:
                                axis_pairs=self._pairs, table_len=self._rope[0].shape[0],
                                grad_dtype=grad_dtype)
         at = first_frame * self.tf
+        if first_frame < 0 or at + tokens > self._pos.shape[0]:
+            raise ValueError(f"tokens {at} to {at + tokens} are not in the {self._pos.shape[0]} that have positions")
         return cfg, self._pos[at:at + tokens].expand(self.B, -1, -1).contiguous()
 
     def norm_rope(self, q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, first_frame: int):

@@ -60,3 +60,20 @@ def test_a_first_call_that_is_captured(cuda_dev, B):
     graph.replay()
     assert all(torch.equal(u, v) for u, v in zip(out, want))
     assert int(a.status.item()) == 0
+
+
+def test_frames_past_the_table_are_refused(cuda_dev):
+    """Their outputs would be left unwritten.  The last frames of the table are not refused."""
+    a = attention(cuda_dev, H=2, D=64, fh=4, fw=8, frames=10)
+    g = torch.Generator().manual_seed(2)
+    x = heads(cuda_dev, g, a, 2)
+    for first in (-1, 9, 10, 10 ** 9):
+        with pytest.raises(ValueError):
+            a.norm_rope(*x[:4], first)
+        with pytest.raises(ValueError):
+            a.norm_rope_backward(*x[:4], first, *x[4:])
+    q, k = a.norm_rope(*x[:4], 8)
+    assert torch.isfinite(q).all() and int(a.status.item()) == 0
+    # what a table starts with does not depend on its length
+    b = attention(cuda_dev, H=2, D=64, fh=4, fw=8, frames=40)
+    assert all(torch.equal(u, v) for u, v in zip((q, k), b.norm_rope(*x[:4], 8)))
