@@ -248,4 +248,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "token_calls", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_token_calls() { return PyModule_Create(&module); }
+// The torch whose tensors this reads: pbsa.py takes no other's, build.py builds again for another.
+#define MARK "token_calls for torch "
+const char* const mark = MARK TORCH_VERSION_BUILT;
+
+PyMODINIT_FUNC PyInit_token_calls() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", mark + sizeof(MARK) - 1)) Py_CLEAR(m);
+    return m;
+}

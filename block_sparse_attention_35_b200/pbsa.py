@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import types
+import warnings
 
 import torch
 
@@ -188,7 +190,25 @@ def _load():
 
 _lib = _load()
 
-from . import token_calls as _calls  # noqa: E402  (built with the library)
+# of csrc/token_calls.cpp, where it makes no call: ctypes then makes all of them
+_NO_CALLS = types.SimpleNamespace(**{name: lambda *args: None for name in (
+    "qk_norm_rope", "qk_norm_rope_bwd", "kv4_append", "kv4_read", "kv4_attn", "kv4_evict")})
+
+
+def _quick_calls():
+    """The module built beside the library, which reads torch's tensors and so belongs to one torch."""
+    try:
+        from . import token_calls
+        if token_calls.torch_version == torch.__version__:
+            return token_calls
+        why = f"was built for torch {token_calls.torch_version}"
+    except ImportError as e:
+        why = str(e)
+    warnings.warn(f"token_calls.so {why}: the token operators' calls go through ctypes (a few us more each)")
+    return _NO_CALLS
+
+
+_calls = _quick_calls()
 
 
 def header_symbols(path: str = HEADER):

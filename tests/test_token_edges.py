@@ -1,8 +1,14 @@
 """Edges of the token operators that need no GPU: sources, refusals, the binding and its build."""
 import os
 import re
+import subprocess
+import sys
 
 import pytest
+import torch
+
+from block_sparse_attention_35_b200 import build as B
+from block_sparse_attention_35_b200 import pbsa as P
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "block_sparse_attention_35_b200", "csrc")
@@ -34,3 +40,54 @@ def test_products_end_before_tensor_memory_is_released():
         barrier = tail.rfind("    tc_fence_before();\n    __syncthreads();")
         drain = tail[barrier:]
         assert "if (s_abort)" in drain and "umma_commit(&s_drain" in drain and "mbar_wait_drain(&s_drain" in drain
+
+
+def test_the_package_imports_without_the_module_of_quick_calls():
+    """Block attention and the token operators do not depend on the module that reads torch's
+    tensors: without it, or with another torch's, ctypes makes the calls."""
+    code = """
+import sys, types, warnings
+warnings.simplefilter("error")
+name = "block_sparse_attention_35_b200.token_calls"
+sys.modules[name] = {stand_in}
+try:
+    import block_sparse_attention_35_b200.pbsa
+except UserWarning as w:
+    assert "ctypes" in str(w), w
+else:
+    raise SystemExit("no warning")
+warnings.simplefilter("ignore")
+import torch
+import block_sparse_attention_35_b200.pbsa as P
+import block_sparse_attention_35_b200.attention, block_sparse_attention_35_b200.token_cache
+c = P.make_kv4_config(1, 2, 2, 64, 64)
+pos, mass = torch.zeros(1, 2, 64, dtype=torch.int32), torch.zeros(1, 2, 64)
+try:
+    P.pbsa_kv4_evict(c, pos, mass, 0, None, pos[..., :1].contiguous(), torch.zeros(1, dtype=torch.int32))
+except P.PBSAError as e:
+    assert "not on a CUDA device" in str(e), e
+else:
+    raise SystemExit("not refused")
+"""
+    for stand_in in ("None", "types.SimpleNamespace(torch_version='1.0')"):
+        r = subprocess.run([sys.executable, "-c", code.replace("{stand_in}", stand_in)], cwd=ROOT,
+                           capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_another_torch_means_another_build(monkeypatch):
+    monkeypatch.setattr(B.os.path, "getmtime", lambda path: 0.0)
+    assert P._calls.torch_version == torch.__version__ and B.calls_up_to_date()
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert not B.calls_up_to_date() and not B.up_to_date()
+
+
+def test_a_module_that_cannot_be_built_is_left_out(monkeypatch, tmp_path):
+    stale = tmp_path / "token_calls.so"
+    stale.write_bytes(b"of another torch")
+    monkeypatch.setattr(B, "CALLS", str(stale))
+    monkeypatch.setattr(B, "calls_command", lambda: [sys.executable, "-c", "raise SystemExit(1)"])
+    monkeypatch.setattr(B, "library_up_to_date", lambda: True)
+    with pytest.warns(UserWarning, match="could not be built"):
+        assert B.build() == B.LIB
+    assert not stale.exists()
