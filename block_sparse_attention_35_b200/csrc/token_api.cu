@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <utility>
 
 #include "pbsa.h"
 #include "pbsa_internal.cuh"
@@ -42,11 +43,27 @@ int get_strides(pbsa::Strides* out, const int64_t* strides, int i, const char* n
     }
     const int64_t* s = strides + 3 * i;
     for (int k = 0; k < 3; ++k)
-        if (s[k] < 0 || (s[k] * es) % 16 != 0)
+        if (s[k] < 0 || s[k] % (16 / es) != 0)
             return api_failf(PBSA_ERR_ARG, "%s: stride %lld is negative or not a multiple of 16 bytes", name, (long long)s[k]);
     out->b = s[0];
     out->t = s[1];
     out->h = s[2];
+    return PBSA_OK;
+}
+
+// Whether the elements of a [B, T, H, D] output are its own: each stride, from the smallest on,
+// steps over all that the smaller ones reach.
+int check_own(const pbsa::Strides& s, const char* name, int B, int T, int H, int D) {
+    struct { long long stride; int n; } d[3] = {{s.b, B}, {s.t, T}, {s.h, H}};
+    if (d[0].stride > d[1].stride) std::swap(d[0], d[1]);
+    if (d[1].stride > d[2].stride) std::swap(d[1], d[2]);
+    if (d[0].stride > d[1].stride) std::swap(d[0], d[1]);
+    __int128 reach = D;
+    for (const auto& x : d) {
+        if (x.n <= 1) continue;
+        if (x.stride < reach) return api_failf(PBSA_ERR_ARG, "%s: stride %lld lets elements share memory", name, x.stride);
+        reach += (__int128)x.stride * (x.n - 1);
+    }
     return PBSA_OK;
 }
 
@@ -184,6 +201,8 @@ int pbsa_qk_norm_rope(const pbsa_qk_config* cfg, const void* q, const void* k, c
     const int es = element_size(cfg->dtype);
     CHECK(get_strides(&a.sy[0], strides, 2, "q_out", cfg->T, cfg->Hq, cfg->D, es));
     CHECK(get_strides(&a.sy[1], strides, 3, "k_out", cfg->T, cfg->Hkv, cfg->D, es));
+    CHECK(check_own(a.sy[0], "q_out", cfg->B, cfg->T, cfg->Hq, cfg->D));
+    if (cfg->Hkv > 0) CHECK(check_own(a.sy[1], "k_out", cfg->B, cfg->T, cfg->Hkv, cfg->D));
     a.y[0] = q_out;
     a.y[1] = k_out;
     const cudaError_t e = pbsa::launch_qk_fwd(a, static_cast<cudaStream_t>(stream));
@@ -219,6 +238,8 @@ int pbsa_qk_norm_rope_bwd(const pbsa_qk_config* cfg, const void* q, const void* 
         CHECK(get_strides(&a.sg[1], strides, 3, "dk_out", cfg->T, cfg->Hkv, cfg->D, gs));
         CHECK(get_strides(&a.sy[0], strides, 4, "dq", cfg->T, cfg->Hq, cfg->D, es));
         CHECK(get_strides(&a.sy[1], strides, 5, "dk", cfg->T, cfg->Hkv, cfg->D, es));
+        CHECK(check_own(a.sy[0], "dq", cfg->B, cfg->T, cfg->Hq, cfg->D));
+        if (cfg->Hkv > 0) CHECK(check_own(a.sy[1], "dk", cfg->B, cfg->T, cfg->Hkv, cfg->D));
         a.gy[0] = dq_out;
         a.gy[1] = dk_out;
         a.y[0] = dq;

@@ -368,7 +368,8 @@ PBSA_API size_t pbsa_qk_workspace_size(const pbsa_qk_config* cfg);
  *   q, q_out [B, T, Hq, D], k, k_out [B, T, Hkv, D] of cfg->dtype
  *   strides  NULL (all contiguous) or 12 strides in elements: batch, token and head of q, k,
  *            q_out, k_out in that order (channels are contiguous; every stride a multiple of
- *            16 bytes; inputs may be broadcast, with strides of 0).  Views of one projection's
+ *            16 bytes; inputs may be broadcast, with strides of 0; an output's strides nest, each
+ *            past all that the smaller ones reach).  Views of one projection's
  *            output are read in place.  An output may be its own input (same pointer and
  *            strides), else they must not overlap.
  *   wq, wk   nullable (all ones); [D] fp32

@@ -1,4 +1,5 @@
 """Edges of the token operators that need no GPU: sources, refusals, the binding and its build."""
+import ctypes
 import os
 import re
 import subprocess
@@ -91,3 +92,20 @@ def test_a_module_that_cannot_be_built_is_left_out(monkeypatch, tmp_path):
     with pytest.warns(UserWarning, match="could not be built"):
         assert B.build() == B.LIB
     assert not stale.exists()
+
+
+@pytest.mark.parametrize("bad", [
+    (0, 128, 64), (512, 0, 64), (512, 128, 0),        # broadcast
+    (512, 128, 56), (512, 120, 64), (448, 128, 64),   # a head, a token, a sequence over the one before
+    (64, 512, 64), (128, 64, 256),                   # in another order
+    (2 ** 62, 64, 2 ** 62),
+])
+def test_outputs_whose_elements_share_memory_are_refused(bad):
+    """[2, 4, 2, 64] outputs: the good strides are (512, 128, 64)."""
+    lib, qc, good = P.library(), P.make_qk_config(2, 4, 2, 2, 64, table_len=8), (512, 128, 64)
+    for call, n, outputs in ((lib.pbsa_qk_norm_rope, 4, (2, 3)), (lib.pbsa_qk_norm_rope_bwd, 6, (4, 5))):
+        for i in outputs:
+            strides = [s for j in range(n) for s in (bad if j == i else good)]
+            args = [256, 256, (ctypes.c_int64 * len(strides))(*strides)] + [256] * (8 if n == 4 else 12)
+            rc = call(ctypes.byref(qc), *args, *((None,) if n == 4 else (1 << 20, 256, None)))
+            assert rc == P.PBSA_ERR_ARG and "share memory" in P.pbsa_last_error()
