@@ -14,7 +14,7 @@ constexpr int kUnit = 16;      // keys of one tensor-core step: a warp's share o
 constexpr int kBlock = kWarps * kUnit;
 constexpr int kStages = 4;     // blocks in the ring
 constexpr int kMassWarps = 4;
-constexpr int kMassRun = 4, kMassFull = 16 * kSMs * kMassWarps;
+constexpr int kMassRun = 4, kMassFull = 16 * kSMs * kMassWarps;   // see run_attn
 
 // A block of keys in shared memory, as it lies in the cache.
 template <int D>
@@ -108,7 +108,8 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const Keys<D>& x, QF q
 }
 
 // A CTA takes a run of the work list and goes through it segment by segment, a segment being
-// the blocks of one (sequence, key head); all of its rows, at most 8 NT.  One warp asks for block after
+// the blocks of one (sequence, key head) and all of its rows, at most 8 NT: there is one group of
+// rows, and the cursor's head is the key head.  One warp asks for block after
 // block, across segment borders, into a ring in shared memory (bulk copies).  The others take
 // sixteen of a block's keys each; each has its own running maximum, sum and output, which are
 // joined in shared memory at the end of a segment.  A segment that covers its head's keys goes
@@ -562,8 +563,9 @@ __global__ void __launch_bounds__(kMassThreads) mass_logits_kernel(AttnArgs a) {
 // Masses of up to 8 NT rows: the scores are formed again (half of the cache's bytes) once the
 // rows' sums are known; a warp owns its keys and takes all rows, so that every sum has one order
 // and one owner, and a code is turned into fp16 once.  Latency bounds it, so a warp of a large
-// call takes `run` units of keys with the next on its way (32 rows x 32 heads over 8192 cached
-// rows: 17.5 us, 22 with one unit a warp), and the first is read before the wait.
+// call takes `run` units of keys with the next on its way (figures in run_attn), and the first is
+// read before the wait.  The rows' constants lie in shared memory: in registers they took 104 to
+// 138 of them and 3 us more a call (20 and 32 rows x 32 heads over 8192 cached rows).
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a, int run) {
     constexpr int kSteps = D / 16;
@@ -618,9 +620,10 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_kernel(AttnArgs a, int r
     }
 }
 
-// Groups of eight rows that a CTA of attn_kernel takes.  (20 rows x 8 heads of 4 sequences over
-// 8192 cached rows: 32.9 us with three, 37.6 with four.)
-int row_groups(int R) { return R <= 32 ? (R + 7) / 8 : 4; }
+// Groups of eight rows that a CTA of attn_kernel takes: all rows of a key head.  (20 rows x 8 heads
+// of 4 sequences over 8192 cached rows: 34.0 us with three, 37.6 with four.)
+int row_groups(int R) { return (R + 7) / 8; }
+static_assert(kFewRows == 32, "attn_kernel is built for one to four groups of eight rows");
 
 bool keeps_logits(int R) { return R <= 8; }
 
@@ -628,8 +631,8 @@ bool keeps_logits(int R) { return R <= 8; }
 // has less than a block.  Returns the blocks of a full cache.
 long long plan(const pbsa_kv4_config& c, int R, AttnArgs& a) {
     const bool chunk = chunk_takes(R);
-    const int nt = row_groups(R), per_sm = !chunk && nt == 1 ? 2 : 1;
-    a.rows = chunk ? kChunkRows : 8 * nt;
+    const int per_sm = !chunk && row_groups(R) == 1 ? 2 : 1;
+    a.rows = chunk ? kChunkRows : 8 * row_groups(R);
     a.groups = (R + a.rows - 1) / a.rows;
     a.heads = c.Hkv * a.groups;
     a.block = chunk ? kChunkKeys : kBlock;
@@ -687,10 +690,11 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
     const bool chunk = chunk_takes(a.R);
     cudaError_t e;
     if (chunk) e = launch_chunk_attn(a, st);
+    else if (a.groups != 1) return cudaErrorInvalidValue;   // attn_kernel knows no others
     else if (a.rows == 8) e = a.k.mass ? run_rows<D, 1, T, true>(a, st) : run_rows<D, 1, T, false>(a, st);
     else if (a.rows == 16) e = run_rows<D, 2, T, false>(a, st);
     else if (a.rows == 24) e = run_rows<D, 3, T, false>(a, st);
-    else e = run_rows<D, 4, T, false>(a, st);
+    else e = run_rows<D, 4, T, false>(a, st);   // 32: kFewRows
     if (e != cudaSuccess) return e;
     const int bh = a.k.c.B * a.k.c.Hkv;
     const long long rows = (long long)bh * a.R;
@@ -698,7 +702,9 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
         const int per = threads / (parts * D / 4);
         return launch_after(kernel, dim3((unsigned)((rows + per - 1) / per)), threads, 0, st, a);
     };
-    // few heads have many parts each
+    // Few heads have many parts each.  Whole calls, with 1, 4 and 16 parts of a row at a time: 296
+    // parts a head 82.4, 43.9, 18.4 us; 9 parts of 8 rows 23.0, 21.3, 20.8; 4 parts of 8 rows 30.9,
+    // 29.8, 33.6; 2 of 8 48.2, 48.2, 57.3; 1 of 8 82.1, 85.1, 101.2.
     const int parts = a.ctas / (a.k.c.B * a.heads);
     if (parts >= 8) e = join(join_kernel<D, 16, T>, kJoinThreads<D, 16>, 16);
     else if (parts >= 2) e = join(join_kernel<D, 4, T>, kJoinThreads<D, 4>, 4);
@@ -709,7 +715,9 @@ cudaError_t run_attn(const AttnArgs& a, cudaStream_t st) {
         const unsigned runs = (unsigned)((a.k.c.capacity + 4 * kMassThreads - 1) / (4 * kMassThreads));
         return launch_after(mass_logits_kernel, dim3((unsigned)bh, runs), kMassThreads, 0, st, a);
     }
-    // units of sixteen keys that a warp takes: several where all of them fill the GPU
+    // Units of sixteen keys that a warp takes: several where all of them fill the GPU (kMassFull).
+    // Whole calls of 20 rows, with one unit and with four: 8192 units in all 33.4 and 35.6 us, 10240
+    // 38.3 and 37.6, 16384 48.2 and 45.1, 65536 141.6 and 125.1 (eight: 123.9, but 50.5 at 16384).
     const int units = a.k.c.capacity / kUnit, run = (long long)bh * units >= kMassFull ? kMassRun : 1;
     const dim3 grid((unsigned)(bh * ((units + kMassWarps * run - 1) / (kMassWarps * run))));
     auto mass = [&](auto kernel) { return launch_after(kernel, grid, 32 * kMassWarps, 0, st, a, run); };

@@ -120,10 +120,11 @@ __device__ __forceinline__ int used_rows(const AttnArgs& a, int b) {
 __device__ __forceinline__ int blocks_of(const AttnArgs& a, int len) { return (len + a.block - 1) / a.block; }
 
 // The work of a call is the list of all blocks of keys, by sequence, head and block (below
-// 2^31 of them), a head here being one of `groups` groups of rows of a key head: the groups
-// follow one another, so that CTAs side by side read the same keys.  n = min(ctas, total) CTAs share it in runs of `each` blocks or,
-// the first `more` of them, one more.  A warp makes and asks it together: every lane adds up
-// the blocks of its share of the sequences.
+// 2^31 of them), a head here being one of `groups` groups of rows of a key head (one, up to
+// kFewRows): the groups follow one another, so that CTAs side by side read the same keys.
+// n = min(ctas, total) CTAs share it in runs of `each` blocks or, the first `more` of them, one
+// more.  A warp makes and asks it together: every lane adds up the blocks of its share of the
+// sequences.
 struct WorkList {
     int total, n, each, more;
     int per, upto, mine;   // sequences of a lane, blocks of the lanes up to this one, and its own
@@ -250,8 +251,14 @@ cudaError_t launch_after(void (*kernel)(AttnArgs, More...), dim3 grid, int threa
     return cudaLaunchKernelEx(&cfg, kernel, a, more...);
 }
 
-// Many rows (kv4_chunk.cu): whether it takes a call, and its launches.
-bool chunk_takes(int R);
+// Up to so many rows of a key head go to attn_kernel, more to the kernels of kv4_chunk.cu.  With 32
+// rows (4 sequences x 8 heads, 8192 cached rows) attn_kernel takes 40.4 us and chunk_kernel 39.7
+// (54.4 against 79.8 with masses; D = 64: 28.6 against 34.5, 38.6 against 72.0); with 40 rows, of
+// which attn_kernel would need two groups, 56.6 against 40.3 (85 against 80.3).
+constexpr int kFewRows = 32;
+inline bool chunk_takes(int R) { return R > kFewRows; }
+
+// Many rows (kv4_chunk.cu).
 cudaError_t launch_chunk_attn(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_chunk_mass(const AttnArgs& a, cudaStream_t st);
 constexpr int kChunkRows = 256, kChunkKeys = 128;

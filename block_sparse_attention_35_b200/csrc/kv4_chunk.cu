@@ -510,57 +510,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
             // -------------------------------------------------- the cache, into operands
             while (left > 0) {
                 const Segment s = segment();
-            const int key = tid - 256;
-            uint4 kc[kQuarters], vc[kQuarters];
-            uint32_t ks[kQuarters], vs[kQuarters];
-            int pos;
-            auto load = [&](int blk) {
-                const int j = blk * 128 + key;
-                const size_t row = (size_t)s.bh * N + j;
-                pos = j < s.len ? __ldg(a.k.cache.pos + row) : -1;
-#pragma unroll
-                for (int q = 0; q < kQuarters; ++q) {
-                    kc[q] = vc[q] = make_uint4(0, 0, 0, 0);
-                    ks[q] = vs[q] = 0;
-                }
-                if (j < s.len) {
+                const int key = tid - 256;
+                uint4 kc[kQuarters], vc[kQuarters];
+                uint32_t ks[kQuarters], vs[kQuarters];
+                int pos;
+                auto load = [&](int blk) {
+                    const int j = blk * 128 + key;
+                    const size_t row = (size_t)s.bh * N + j;
+                    pos = j < s.len ? __ldg(a.k.cache.pos + row) : -1;
 #pragma unroll
                     for (int q = 0; q < kQuarters; ++q) {
-                        kc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.k_codes + row * (D / 2)) + q);
-                        vc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.v_codes + row * (D / 2)) + q);
-                        ks[q] = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.k_scales + row * (D / 16)) + q);
-                        vs[q] = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.v_scales + row * (D / 16)) + q);
+                        kc[q] = vc[q] = make_uint4(0, 0, 0, 0);
+                        ks[q] = vs[q] = 0;
                     }
-                }
-            };
-            load(s.blk0);
-            for (int i = 0; i < s.tiles; ++i) {
-                const uint32_t t = tile + i;
-                const int st = t & 1;
-                const bool here = pos >= 0;
-                if (ok && t >= 2) ok = wait(&s_kfree[st], ((t >> 1) - 1) & 1);
-                if (!ok) break;
-                TileInfo& inf = info[t % kInfo];
-                inf.bias[key] = here ? 0.f : -INFINITY;
-                inf.pos[key] = here ? pos : kHidden;
-                const unsigned live = __ballot_sync(0xffffffffu, here);
-                const int newest = __reduce_max_sync(0xffffffffu, here ? pos : -1);
-                if (lane == 0) {
-                    inf.live[key >> 5] = live;
-                    inf.newest[key >> 5] = newest;
-                }
+                    if (j < s.len) {
 #pragma unroll
-                for (int q = 0; q < kQuarters; ++q) expand32(sK + st * kTile, key, q, kc[q], here ? ks[q] : 0u);
-                fence_proxy_async_smem();
-                mbar_arrive(&s_kfull[st]);
-                if (t >= 2) ok = wait(&s_vfree[st], ((t >> 1) - 1) & 1);
-                if (!ok) break;
+                        for (int q = 0; q < kQuarters; ++q) {
+                            kc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.k_codes + row * (D / 2)) + q);
+                            vc[q] = __ldg(reinterpret_cast<const uint4*>(a.k.cache.v_codes + row * (D / 2)) + q);
+                            ks[q] = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.k_scales + row * (D / 16)) + q);
+                            vs[q] = __ldg(reinterpret_cast<const uint16_t*>(a.k.cache.v_scales + row * (D / 16)) + q);
+                        }
+                    }
+                };
+                load(s.blk0);
+                for (int i = 0; i < s.tiles; ++i) {
+                    const uint32_t t = tile + i;
+                    const int st = t & 1;
+                    const bool here = pos >= 0;
+                    if (ok && t >= 2) ok = wait(&s_kfree[st], ((t >> 1) - 1) & 1);
+                    if (!ok) break;
+                    TileInfo& inf = info[t % kInfo];
+                    inf.bias[key] = here ? 0.f : -INFINITY;
+                    inf.pos[key] = here ? pos : kHidden;
+                    const unsigned live = __ballot_sync(0xffffffffu, here);
+                    const int newest = __reduce_max_sync(0xffffffffu, here ? pos : -1);
+                    if (lane == 0) {
+                        inf.live[key >> 5] = live;
+                        inf.newest[key >> 5] = newest;
+                    }
 #pragma unroll
-                for (int q = 0; q < kQuarters; ++q) expand32(sV + st * kTile, key, q, vc[q], here ? vs[q] : 0u);
-                fence_proxy_async_smem();
-                mbar_arrive(&s_vfull[st]);
-                if (i + 1 < s.tiles) load(s.blk0 + i + 1);
-            }
+                    for (int q = 0; q < kQuarters; ++q) expand32(sK + st * kTile, key, q, kc[q], here ? ks[q] : 0u);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&s_kfull[st]);
+                    if (t >= 2) ok = wait(&s_vfree[st], ((t >> 1) - 1) & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int q = 0; q < kQuarters; ++q) expand32(sV + st * kTile, key, q, vc[q], here ? vs[q] : 0u);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&s_vfull[st]);
+                    if (i + 1 < s.tiles) load(s.blk0 + i + 1);
+                }
                 finish(s);
             }
         }
@@ -571,145 +571,145 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
         while (left > 0) {
             const Segment s = segment();
             if (x < s.sides) {
-            const int r = s.row0 + tid;
-            const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const uint32_t o_at = tmem + lane_at + 256 + 128 * x;
-            const float fac = a.q_scale[((size_t)s.bh * a.tiles128) * 128 + r];
-            const int lim = row_limit(a, s.b, r);
-            const float lag = kLag / fac;
-            float ref = 0.f, thr = -INFINITY, l = 0.f;   // ref, thr: as in attn_kernel
-            float c0 = kShift;                           // near rows: the exponent of a product of 0
-            bool far = false;                            // some row of the warp is not near (kNear)
-            for (int u = 0; ok && u < 2 * s.tiles; ++u) {
-                const int j = u & 1;
-                ok = wait(&s_sfull[x][j], (n_mine + u / 2) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t s_at = tmem + lane_at + 128 * x + 64 * j;
-                uint32_t raw_s[2][32];
-                tmem_ld32(s_at, raw_s[0]);
-                tmem_ld32(s_at + 32, raw_s[1]);
-                const TileInfo& inf = info[(tile + u / 2) % kInfo];
-                const int newest = max(inf.newest[2 * j], inf.newest[2 * j + 1]);
-                // some row of this warp may not see some token of the step, or none has one (rows
-                // past the last are never read back).  Elsewhere every row sees a token, and
-                // adding -infinity to what a NaN query made of an empty row costs nothing more.
-                const bool causal = __any_sync(0xffffffffu, r < a.R && (newest > lim || newest < 0));
-                tmem_ld_wait();
-                float v[64];
+                const int r = s.row0 + tid;
+                const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+                const uint32_t o_at = tmem + lane_at + 256 + 128 * x;
+                const float fac = a.q_scale[((size_t)s.bh * a.tiles128) * 128 + r];
+                const int lim = row_limit(a, s.b, r);
+                const float lag = kLag / fac;
+                float ref = 0.f, thr = -INFINITY, l = 0.f;   // ref, thr: as in attn_kernel
+                float c0 = kShift;                           // near rows: the exponent of a product of 0
+                bool far = false;                            // some row of the warp is not near (kNear)
+                for (int u = 0; ok && u < 2 * s.tiles; ++u) {
+                    const int j = u & 1;
+                    ok = wait(&s_sfull[x][j], (n_mine + u / 2) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t s_at = tmem + lane_at + 128 * x + 64 * j;
+                    uint32_t raw_s[2][32];
+                    tmem_ld32(s_at, raw_s[0]);
+                    tmem_ld32(s_at + 32, raw_s[1]);
+                    const TileInfo& inf = info[(tile + u / 2) % kInfo];
+                    const int newest = max(inf.newest[2 * j], inf.newest[2 * j + 1]);
+                    // some row of this warp may not see some token of the step, or none has one (rows
+                    // past the last are never read back).  Elsewhere every row sees a token, and
+                    // adding -infinity to what a NaN query made of an empty row costs nothing more.
+                    const bool causal = __any_sync(0xffffffffu, r < a.R && (newest > lim || newest < 0));
+                    tmem_ld_wait();
+                    float v[64];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(raw_s[e >> 5][e & 31]);
-                // -infinity for what the row does not see
-                if (causal) {
+                    for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(raw_s[e >> 5][e & 31]);
+                    // -infinity for what the row does not see
+                    if (causal) {
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const int4 q = *reinterpret_cast<const int4*>(&inf.pos[64 * j + e]);
-                        v[e] = q.x <= lim ? v[e] : -INFINITY;
-                        v[e + 1] = q.y <= lim ? v[e + 1] : -INFINITY;
-                        v[e + 2] = q.z <= lim ? v[e + 2] : -INFINITY;
-                        v[e + 3] = q.w <= lim ? v[e + 3] : -INFINITY;
+                        for (int e = 0; e < 64; e += 4) {
+                            const int4 q = *reinterpret_cast<const int4*>(&inf.pos[64 * j + e]);
+                            v[e] = q.x <= lim ? v[e] : -INFINITY;
+                            v[e + 1] = q.y <= lim ? v[e + 1] : -INFINITY;
+                            v[e + 2] = q.z <= lim ? v[e + 2] : -INFINITY;
+                            v[e + 3] = q.w <= lim ? v[e + 3] : -INFINITY;
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (inf.live[2 * j + c] != 0xffffffffu) {
+#pragma unroll
+                                for (int e = 32 * c; e < 32 * c + 32; e += 4) {
+                                    const float4 q = *reinterpret_cast<const float4*>(&inf.bias[64 * j + e]);
+                                    const float2 y = split(add2(pair(v[e], v[e + 1]), pair(q.x, q.y)));
+                                    const float2 z = split(add2(pair(v[e + 2], v[e + 3]), pair(q.z, q.w)));
+                                    v[e] = y.x, v[e + 1] = y.y, v[e + 2] = z.x, v[e + 3] = z.y;
+                                }
+                            }
                     }
-                } else {
+                    float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        if (inf.live[2 * j + c] != 0xffffffffu) {
+                    for (int e = 4; e < 64; e += 8) {
 #pragma unroll
-                            for (int e = 32 * c; e < 32 * c + 32; e += 4) {
-                                const float4 q = *reinterpret_cast<const float4*>(&inf.bias[64 * j + e]);
-                                const float2 y = split(add2(pair(v[e], v[e + 1]), pair(q.x, q.y)));
-                                const float2 z = split(add2(pair(v[e + 2], v[e + 3]), pair(q.z, q.w)));
-                                v[e] = y.x, v[e + 1] = y.y, v[e + 2] = z.x, v[e + 3] = z.y;
+                        for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], e + 4 + k < 64 ? fmaxf(v[e + k], v[e + 4 + k]) : v[e + k]);
+                    }
+                    const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    const bool grow = t > thr;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float k = !grow ? 1.f : (thr == -INFINITY ? 0.f : ex2((ref - t) * fac));
+                        if (u > 0) {
+                            ok = wait(&s_pv[x][(u - 1) & 1], (n_mine + (u - 1) / 2) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t y[16];
+                                tmem_ld16(o_at + 16 * c, y);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * k);
+                                tmem_st16(o_at + 16 * c, y);
+                            }
+                            tmem_st_wait();
+                        }
+                        if (grow) {
+                            l *= k;
+                            ref = t;
+                            thr = __fadd_rd(t, lag);
+                        }
+                        far = __any_sync(0xffffffffu, fabsf(ref * fac) >= kNear);
+                        c0 = far ? kShift : fmaf(-ref, fac, kShift);
+                    }
+                    if (far) {
+                        const uint64_t m2 = pair(-ref, -ref);
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const float2 y = split(add2(pair(v[e], v[e + 1]), m2));
+                            v[e] = y.x, v[e + 1] = y.y;
+                        }
+                    }
+                    const uint64_t fac2 = pair(fac, fac), c2 = pair(c0, c0);
+                    uint64_t part[2] = {0, 0};
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float2 y = split(fma2(pair(v[2 * e], v[2 * e + 1]), fac2, c2));
+                        y.x = ex2(y.x), y.y = ex2(y.y);
+                        part[e & 1] = add2(part[e & 1], pair(y.x, y.y));
+                        const __half2 h = __floats2half2_rn(y.x, y.y);
+                        p[e] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    tmem_st32(s_at, p);   // over products that have been read
+                    const float2 sums = split(add2(part[0], part[1]));
+                    l += sums.x + sums.y;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&s_pfull[x][j]);
+                }
+                if (ok) ok = wait(&s_pv[x][1], (n_mine + s.tiles - 1) & 1);   // an even number of steps
+                if (ok) {
+                    tc_fence_after();
+                    const bool whole = s.blk0 == 0 && s.tiles == s.nblk;
+                    const size_t slot = ((size_t)blockIdx.x * 2 + (s.blk0 == 0)) * kChunkRows + tid;
+                    const int tt = r / a.G, h = s.hkv * a.G + r - tt * a.G;
+                    T* out = static_cast<T*>(a.k.out) + (((size_t)s.b * a.k.T + tt) * a.k.c.Hq + h) * D;
+                    const float inv = l == 0.f ? 0.f : a.k.c.v_unit / l;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(o_at + 32 * c, v);
+                        tmem_ld_wait();
+                        if (r < a.R) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                float4 y = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                                       __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                                if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (whole) store4(out + 32 * c + e, y, inv);
+                                else *reinterpret_cast<float4*>(a.part_o + slot * D + 32 * c + e) = y;
                             }
                         }
-                }
-                float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                for (int e = 4; e < 64; e += 8) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], e + 4 + k < 64 ? fmaxf(v[e + k], v[e + 4 + k]) : v[e + k]);
-                }
-                const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                const bool grow = t > thr;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float k = !grow ? 1.f : (thr == -INFINITY ? 0.f : ex2((ref - t) * fac));
-                    if (u > 0) {
-                        ok = wait(&s_pv[x][(u - 1) & 1], (n_mine + (u - 1) / 2) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t y[16];
-                            tmem_ld16(o_at + 16 * c, y);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * k);
-                            tmem_st16(o_at + 16 * c, y);
-                        }
-                        tmem_st_wait();
                     }
-                    if (grow) {
-                        l *= k;
-                        ref = t;
-                        thr = __fadd_rd(t, lag);
-                    }
-                    far = __any_sync(0xffffffffu, fabsf(ref * fac) >= kNear);
-                    c0 = far ? kShift : fmaf(-ref, fac, kShift);
-                }
-                if (far) {
-                    const uint64_t m2 = pair(-ref, -ref);
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const float2 y = split(add2(pair(v[e], v[e + 1]), m2));
-                        v[e] = y.x, v[e + 1] = y.y;
-                    }
-                }
-                const uint64_t fac2 = pair(fac, fac), c2 = pair(c0, c0);
-                uint64_t part[2] = {0, 0};
-                uint32_t p[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float2 y = split(fma2(pair(v[2 * e], v[2 * e + 1]), fac2, c2));
-                    y.x = ex2(y.x), y.y = ex2(y.y);
-                    part[e & 1] = add2(part[e & 1], pair(y.x, y.y));
-                    const __half2 h = __floats2half2_rn(y.x, y.y);
-                    p[e] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                tmem_st32(s_at, p);   // over products that have been read
-                const float2 sums = split(add2(part[0], part[1]));
-                l += sums.x + sums.y;
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&s_pfull[x][j]);
-            }
-            if (ok) ok = wait(&s_pv[x][1], (n_mine + s.tiles - 1) & 1);   // an even number of steps
-            if (ok) {
-                tc_fence_after();
-                const bool whole = s.blk0 == 0 && s.tiles == s.nblk;
-                const size_t slot = ((size_t)blockIdx.x * 2 + (s.blk0 == 0)) * kChunkRows + tid;
-                const int tt = r / a.G, h = s.hkv * a.G + r - tt * a.G;
-                T* out = static_cast<T*>(a.k.out) + (((size_t)s.b * a.k.T + tt) * a.k.c.Hq + h) * D;
-                const float inv = l == 0.f ? 0.f : a.k.c.v_unit / l;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(o_at + 32 * c, v);
-                    tmem_ld_wait();
                     if (r < a.R) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 y = make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                                                   __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-                            if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (whole) store4(out + 32 * c + e, y, inv);
-                            else *reinterpret_cast<float4*>(a.part_o + slot * D + 32 * c + e) = y;
-                        }
+                        if (whole) finish_sum(a, s.b, s.hkv, r, tt, h, ref, fac, l);
+                        else a.part_ml[slot] = make_float4(thr == -INFINITY ? -INFINITY : ref, l, fac, 0.f);
                     }
                 }
-                if (r < a.R) {
-                    if (whole) finish_sum(a, s.b, s.hkv, r, tt, h, ref, fac, l);
-                    else a.part_ml[slot] = make_float4(thr == -INFINITY ? -INFINITY : ref, l, fac, 0.f);
-                }
-            }
                 n_mine += s.tiles;
             }
             finish(s);
@@ -734,11 +734,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(AttnArgs a) {
 }
 
 }  // namespace
-
-// With 32 rows (4 sequences x 8 heads, 8192 cached rows) attn_kernel takes 39.5 us and
-// chunk_kernel 39.8 (57 against 74 with masses); with 40 rows, of which attn_kernel needs two
-// groups, 56.6 against 40.3 (85 against 75).
-bool chunk_takes(int R) { return R > 32; }
 
 cudaError_t launch_chunk_attn(const AttnArgs& a, cudaStream_t st) {
     auto run = [&](auto prep, auto kernel, int D) -> cudaError_t {
