@@ -346,6 +346,9 @@ PBSA_API int pbsa_cache_update(const pbsa_config* cfg, const void* k_local, cons
  * and column for video): the first axis_pairs[0] pairs turn by component 0, the next
  * axis_pairs[1] by component 1, and so on.  Pair i of a token at component p turns by the
  * angle whose cosine and sine are cos[p][i] and sin[p][i].
+ *
+ * The squares are summed in fp32, as the rest is: a head with an entry above 2^60 (1.1e18; bf16 and
+ * fp32 hold such) may have a sum past fp32's range, and then r = 0.
  */
 typedef struct pbsa_qk_config {
     int B, T;            /* sequences, tokens of each (0 is allowed) */
@@ -432,7 +435,9 @@ typedef struct pbsa_kv4_cache {
 } pbsa_kv4_cache;
 
 PBSA_API int pbsa_validate_kv4_config(const pbsa_kv4_config* cfg);
-/* Workspace bytes of pbsa_kv4_attn for T query tokens (0 on a bad configuration). */
+/* Workspace bytes of pbsa_kv4_attn for T query tokens, with masses or without (0 on a bad
+ * configuration).  Up to 8 query rows a key head, 4 bytes of it for each of them and each of the
+ * cache's rows serve the masses alone. */
 PBSA_API size_t pbsa_kv4_workspace_size(const pbsa_kv4_config* cfg, int T);
 
 /*
@@ -467,13 +472,19 @@ PBSA_API int pbsa_kv4_read(const pbsa_kv4_config* cfg, const pbsa_kv4_cache* cac
 /*
  * Attention of T query tokens of every sequence over its cache, softmax scale 1/sqrt(D).
  *
+ * Queries are scaled row by row by a power of two and held in fp16, with an error of at most 2^-39
+ * of the row's largest entry (none in fp16's or bf16's entries down to 2^-31 of it); probabilities
+ * are rounded to fp16 (2^-11 of each) before they are multiplied with the values.  Products' sums,
+ * maxima, the probabilities' sums, outputs and masses are fp32.  Logits of any size keep their
+ * differences, as far as an fp32 sum of products holds them; an lse past fp32 is infinite.
+ *
  * Row j of (b, key head) is seen by query t when j < kv_len[b], pos[j] >= 0 and, with q_pos,
  * pos[j] <= q_pos[b][t].  A query that sees no row (an empty cache; q_pos -1, the padding of a
  * shorter sequence) gets out = 0 and lse = -infinity and adds nothing to the masses, whatever it
  * holds.  A NaN or an infinity in a query that sees rows makes its own output NaN, and the masses
  * of the rows it sees.
  *
- *   q        [B, T, Hq, D]; strides NULL or 3 (batch, token, head)
+ *   q        [B, T, Hq, D]; strides NULL or 3 (batch, token, head); out does not overlap it
  *   q_pos    nullable; [B, T] int32, the causal mask above
  *   kv_len   [B] int32: rows in use; outside [0, N] it is clamped and PBSA_ERR_DEVICE_CHECK
  *            recorded
