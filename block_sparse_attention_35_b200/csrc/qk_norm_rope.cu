@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* partial, int b
 
 // Heads of one work item: all of a token's heads when the tokens alone fill the GPU (the
 // rotation is then loaded once per token), else as few as still give every resident warp
-// (`ctas` blocks an SM) an item of its own, down to the heads of one step.
+// (`ctas` blocks an SM) an item of its own, down to the heads of one step.  Of at least one token.
 int heads_per_item(const pbsa_qk_config& c, int ctas) {
     const int heads = c.Hq + c.Hkv, step = 32 / (c.D / 8);
     const long long tokens = (long long)c.B * c.T, warps = (long long)kSMs * kWarps * ctas;
@@ -405,9 +405,9 @@ cudaError_t run_fwd(const QkArgs& a, cudaStream_t st) {
 
 template <typename T, typename G, int D, bool IL>
 cudaError_t run_bwd(const QkArgs& a, cudaStream_t st) {
-    const int per = heads_per_item(a.c, kBwdCtas), ipt = (a.c.Hq + a.c.Hkv + per - 1) / per;
-    const int blocks = qk_bwd_blocks(a.c);
+    const int blocks = qk_bwd_blocks(a.c);   // 0 without tokens: the weights' gradients are zeros then
     if (blocks > 0) {
+        const int per = heads_per_item(a.c, kBwdCtas), ipt = (a.c.Hq + a.c.Hkv + per - 1) / per;
         qk_bwd_kernel<T, G, D, IL><<<blocks, 32 * kWarps, 0, st>>>(a, per, ipt);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -109,3 +109,31 @@ def test_outputs_whose_elements_share_memory_are_refused(bad):
             args = [256, 256, (ctypes.c_int64 * len(strides))(*strides)] + [256] * (8 if n == 4 else 12)
             rc = call(ctypes.byref(qc), *args, *((None,) if n == 4 else (1 << 20, 256, None)))
             assert rc == P.PBSA_ERR_ARG and "share memory" in P.pbsa_last_error()
+
+
+def test_a_call_without_tokens_divides_by_none(tmp_path):
+    """The split of the heads divides by the tokens, which an optimising compiler may hide: the host
+    code of a call without tokens is run as it is written."""
+    src = open(os.path.join(CSRC, "qk_norm_rope.cu")).read()
+    body = src[src.index("int heads_per_item("):]
+    split = body[:body.index("\n}\n") + 3]
+    blocks = src[src.index("int qk_bwd_blocks("):]
+    blocks = blocks[:blocks.index("\n}\n") + 3]
+    run = src[src.index("cudaError_t run_bwd("):]
+    run = run[run.index("{") + 1:run.index("\n}\n")]
+    run = re.sub(r"qk_\w+<[^;]*;", ";", run)           # no launches
+    (tmp_path / "t.cpp").write_text("""
+#include "pbsa.h"
+typedef int cudaError_t; enum { cudaSuccess = 0 }; int cudaGetLastError() { return 0; }
+constexpr int kSMs = 148, kWarps = 8, kFwdCtas = 4, kBwdCtas = 2, D = 64;
+struct QkArgs { pbsa_qk_config c; float* dw[2]; };
+""" + split + blocks + "int run(const QkArgs& a) {" + run + """}
+int main() {
+    QkArgs a{};
+    a.c.B = 1, a.c.T = 0, a.c.Hq = 2, a.c.Hkv = 2, a.c.D = D;
+    return run(a);
+}
+""")
+    exe = str(tmp_path / "t")
+    subprocess.run(["g++", "-O0", "-w", "-I", os.path.join(ROOT, "include"), "-o", exe, str(tmp_path / "t.cpp")], check=True)
+    assert subprocess.run([exe], timeout=60).returncode == 0
