@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), NT == 1 ? 2 : 1) attn_kerne
         auto fac = [&](int n, int i) -> float { return NT == 1 ? fac1[i] : fac_sm[8 * n + 2 * c + i]; };
         auto lim = [&](int n, int i) -> int { return NT == 1 ? lim1[i] : lim_sm[8 * n + 2 * c + i]; };
         auto qf = [&](int j, int n) -> uint2 { return NT == 1 ? qr[NT == 1 ? j : 0] : q_sm[(j * NT + n) * 32 + lane]; };
-        const bool choosy = a.k.q_pos || kRows > a.R;   // some row may not see some key
+        const bool choosy = a.k.q_pos;   // some row may not see some key (rows past the last, zeros, may see all)
         float* lg = kLogits ? a.logits + ((size_t)bh * a.R + 2 * c) * N + g : nullptr;
 
         float ref[NT][2], thr[NT][2], l[NT][2], o[NT][kSteps][4];
