@@ -52,6 +52,7 @@ class TokenCache:
         self.kv_len = torch.zeros(B, **i32)     # rows in use
         self.status = torch.zeros(1, **i32)
         self._count = torch.arange(capacity, **i32)
+        self._turn = torch.arange(capacity, device=dev) - capacity
         self._steps = {}                        # by T: see _buffers
 
     def _buffers(self, T: int):
@@ -100,17 +101,18 @@ class TokenCache:
         n = T
         if n_new is not None:
             n = n_new.clamp(0, T).int()
-            pos = torch.where(s["ar"] < n[:, None], pos, torch.full_like(pos, -1))
+            pos = torch.where(s["ar"] < n[:, None], pos, -1)
         P.pbsa_kv4_evict(self.cfg, self.pos, self.mass, self.n_sink, self.seen - self.n_recent,
                          s["rows"], self.status)
         rows = s["rows"]
-        if n_new is not None:   # empty rows first: the last of them may stand behind rows in use
-            used = self.pos.gather(2, rows.clamp(min=0).long()) >= 0
-            rows = rows.gather(2, used.int().argsort(dim=-1, stable=True))
+        if n_new is not None and T > 1:
+            # Empty rows first.  The rows in use are the first kv_len, so that of the T chosen ones,
+            # in row order, the last capacity - kv_len are empty: they are turned to the front.
+            turn = (self._turn[:T] + self.kv_len.clamp(min=self.capacity - T)[:, None]) % T
+            rows = rows.gather(2, turn[:, None].expand(rows.shape))
         P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, rows, self.mass, self.status)
         self.seen += n
-        self.kv_len += n
-        self.kv_len.clamp_(max=self.capacity)
+        torch.clamp(self.seen, max=self.capacity, out=self.kv_len)
         P.pbsa_kv4_attn(self.cfg, self.cache, q, pos, self.kv_len, s["out"], s["lse"], self.mass,
                         s["ws"], self.status)
         return s["out"]
