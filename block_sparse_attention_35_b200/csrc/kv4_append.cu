@@ -16,8 +16,10 @@
 // append_kernel and read_kernel are bound by HBM: one thread owns one block of sixteen
 // channels, 32 bytes of a 16-bit type against 8 bytes of codes and one scale byte; neighbouring
 // threads own neighbouring blocks, so a warp touches whole sectors on both sides.  4680 tokens
-// of 12 heads of 128 channels, L2 cold: append 11.8 us (28.8 MB read, 8.1 MB written, to
-// scattered rows), read 10.3 us; one token of 32 x 8 caches 2.9 and 2.6 us, launch and latency.
+// of 12 heads of 128 channels, L2 cold: append 11.6 us (28.8 MB read, 8.1 MB written, to
+// scattered rows), read 10.5 us; 18720 tokens 32.3 and 36.1 us, so 4 us are fixed (launch, the
+// first look-ups) and the rest streams at 5.3 and 4.5 TB/s: a thread waits for its row's place
+// before it can store (append) or load (read).  One token of 32 x 8 caches 2.7 and 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -119,14 +119,19 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const Keys<D>& x, QF q
 // so that rows come in groups of eight and a code is turned into fp16 once, in the register
 // that it is multiplied from.
 //
-// What bounds it (D = 128, L2 cold).  A step of sixteen keys is 2.4 KB and 331 instructions of a
-// warp, 161 of them on the ALU pipe that takes one every other cycle (64 conversions of code
-// pairs): with fourteen computing warps an SM, long caches stream at 4.9 TB/s, three quarters of
+// What bounds it (D = 128, L2 cold).  A step of sixteen keys is 2.4 KB and 338 instructions of a
+// warp, 163 of them on the ALU pipe that takes one every other cycle (64 conversions of code
+// pairs): with fourteen computing warps an SM, long caches stream at 4.7 TB/s, three quarters of
 // the copy rate.  Without any arithmetic the same ring streams at 7.4 TB/s, so the ring does not
-// bound it.  Short calls are latency: lengths, list, first blocks, the join.
-//   131072 rows x 4 heads, 8 query rows: 30 us a call (77.6 MB), of which 14 are fixed;
-//   32 ragged sequences x 8 heads, 4 rows, with masses: 72 us (168 MB);
-//   4096 rows x 12 heads, 1 row: 11.7 us.
+// bound it.  Short calls are latency.
+//   131072 rows x 4 heads, 8 query rows: 30 us a call (77.6 MB).  4.0 of them without a key (two
+//   launches), 6.8 more for the first block of every CTA and the join of 74 parts, 1.0 to 1.2 for
+//   each of the 15 blocks after it.
+//   32 sequences x 8 heads of 4224 rows, 4 query rows: 50 us (160 MB); of ragged lengths (4200 on
+//   average) 58, as CTAs on the short ones end a segment every few blocks, with its join in shared
+//   memory and new queries, 2 to 3 us each.  One query row in place of four: the same.  Masses
+//   add 8 (kept products and the pass over them).
+//   4096 rows x 12 heads, 1 row: 11.8 us.
 // Measured and left: eight computing warps that issue the loads in turn, 33.7 against 30.7 us for
 // each further 155 MB; two steps a warp at a time, whose chains overlap, and nine computing warps
 // with the queries in shared memory, neither faster.

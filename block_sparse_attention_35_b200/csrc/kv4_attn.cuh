@@ -25,7 +25,8 @@ constexpr float kShift = 7.f;
 constexpr float kLag = 8.f;
 // Where a row's largest base-2 logit is below this, the difference may as well be formed by the
 // multiply-add that scales it: rounding the constant costs no more than 2^-24 of the logit, which
-// its product has lost already, and one instruction less for every score.
+// its product has lost already, and it is one instruction less for every score (chunk_kernel; the
+// other kernels have room for it and always subtract).
 constexpr float kNear = 256.f;
 
 // The T tokens x G query heads of one key head are the R = T G rows that share its keys; a CTA

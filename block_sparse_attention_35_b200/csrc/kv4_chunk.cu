@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(256) prep_kernel(AttnArgs a) {
 // A CTA owns 128 keys of a (sequence, key head) and walks all rows, 128 at a time, through two
 // buffers in shared and tensor memory; two groups of four warps take the row tiles in turn.
 // Tensor memory is read as products of mma.sync lie, four keys and a quarter of the columns a
-// lane: the columns' factors and lse cost a quarter of the shared-memory loads that a lane per
-// key would take (141 against 138 us).
+// lane: the columns' constants cost a quarter of the shared-memory loads that a lane per key would
+// take (141 against 138 us, before the references were products).
 // Bound by the exponentials (one a key and row, 16 a clock and SM: 80 us for 1560 rows x 12
-// heads x 18752 keys); it takes 138 us: 8.8 us for each 128 rows (73 % of that rate) and 23 for
-// the starts of six rounds of CTAs (expanding the keys).  A quarter of the exponentials as
+// heads x 18752 keys); it takes 135 us: 8.5 us for each 128 rows (three quarters of that rate) and
+// 25 for the starts of six rounds of CTAs (expanding the keys).  A quarter of the exponentials as
 // polynomials on the FMA pipe changed nothing, here and in chunk_kernel; half of them cost 17 us
 // here and 13 there.  The mma.sync form that preceded it took 630 us.
 constexpr int kMassGroupThreads = 320;   // 8 warps that compute, one that loads, one that issues
@@ -331,12 +331,14 @@ __global__ void __launch_bounds__(kMassGroupThreads, 2) chunk_mass_kernel(AttnAr
 // own S and is the A operand of PV.  (Products of different shapes may overlap: QK waits until
 // PV is done.)
 //
-// 1560 rows x 12 heads over 18752 rows, D = 128: 225 us for 180 GFLOP (0.80 PFLOP/s).  The
+// 1560 rows x 12 heads over 18752 rows, D = 128: 230 us for 180 GFLOP (0.78 PFLOP/s).  The
 // softmax sets the pace: of the 2300 cycles of a step (at 237 us) its warps waited 200 to 500 for
 // scores; the rest was reading them (140), hiding rows without a token (400), the maximum (220)
 // and the exponentials (1100, two warps to a scheduler).  With 128 keys a step and one S (and a
 // second sweep over it) the kernel took 307 us, with one warp issuing both sides 243, without
-// pairs 236.  A last group of at most 128 rows takes nearly as long as a whole one (29 us each).
+// pairs 236.  A last group of at most 128 rows takes nearly as long as a whole one (30 us each).
+// Near rows (kNear) keep one multiply-add a score: 239.7 us for such a call without masses, 250.0
+// where every warp takes its rows for far ones.
 constexpr int kChunkThreads = 14 * 32;
 constexpr int kInfo = 4;   // tiles whose key info is kept: a softmax is at most two tiles behind
 

@@ -21,11 +21,15 @@
 // block in shared memory, and the blocks' sums are added by a second small kernel in a fixed
 // order (no atomics), all in 32 bits.
 //
-// 32760 tokens of 12 + 12 heads of 128 bf16 channels, three axes, L2 cold: forward 73 us
-// (403 MB, 5.5 TB/s), backward with fp32 gradients 135 us (604 MB, 4.5 TB/s: 128 registers leave
-// 16 warps an SM, and what they have in flight bounds it; with two steps of loads in flight in
-// place of three 147 us, with the weights in shared memory and the next step's loads behind this
-// step's work 152), weights' sums 3 us.
+// 32760 tokens of 12 + 12 heads of 128 channels, three axes, L2 cold; the backward with the weights'
+// sums (3 us):
+//   bf16, fp32 gradients   forward 73 us (403 MB, 5.5 TB/s), backward 137 (805 MB, 5.9 TB/s)
+//   fp16, fp16 gradients   73, and 122 (604 MB, 5.0 TB/s)
+//   fp32                   125 (805 MB, 6.4 TB/s), and 223 (1.21 GB, 5.4 TB/s)
+// (a copy runs at 6.5).  In the backward 128 registers leave 16 warps an SM, and what they have in
+// flight bounds it where the gradients are narrow: with two steps of loads in flight in place of
+// three 147 us, with the weights in shared memory and the next step's loads behind this step's work
+// 152.  A step of fp32 is twice the registers: one is in flight in the backward, two in the forward.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
