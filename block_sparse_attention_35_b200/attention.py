@@ -159,7 +159,8 @@ class SparseForcingAttention:
         at = first_frame * self.tf
         if first_frame < 0 or at + tokens > self._pos.shape[0]:
             raise ValueError(f"tokens {at} to {at + tokens} are not in the {self._pos.shape[0]} that have positions")
-        return cfg, self._pos[at:at + tokens].expand(self.B, -1, -1).contiguous()
+        pos = self._pos[at:at + tokens].expand(self.B, -1, -1).contiguous()
+        return cfg, pos.clone() if pos.data_ptr() % 16 else pos   # frames of odd sizes
 
     def norm_rope(self, q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, first_frame: int):
         """RMS-normalises every head of the projected queries and keys [B, frames*T_f, H, D]

@@ -77,3 +77,22 @@ def test_frames_past_the_table_are_refused(cuda_dev):
     # what a table starts with does not depend on its length
     b = attention(cuda_dev, H=2, D=64, fh=4, fw=8, frames=40)
     assert all(torch.equal(u, v) for u, v in zip((q, k), b.norm_rope(*x[:4], 8)))
+
+
+@pytest.mark.parametrize("B", [1, 2])
+@pytest.mark.parametrize("fh,fw", [(3, 5), (2, 3), (9, 7)])
+def test_frames_of_odd_sizes(cuda_dev, B, fh, fw):
+    """Positions of a later frame begin at any multiple of 12 bytes; two frames at once are the two
+    one by one."""
+    a = attention(cuda_dev, B=B, H=2, D=64, fh=fh, fw=fw, frames=12)
+    g = torch.Generator().manual_seed(3)
+    q, k, wq, wk, gq, gk = heads(cuda_dev, g, a, 2)
+    one = lambda t, i: t[:, i * a.tf:(i + 1) * a.tf]
+    for first in range(5):
+        both = (*a.norm_rope(q, k, wq, wk, first), *a.norm_rope_backward(q, k, wq, wk, first, gq, gk)[:2])
+        for i in range(2):
+            x = [one(t, i) for t in (q, k, gq, gk)]
+            got = (*a.norm_rope(*x[:2], wq, wk, first + i),
+                   *a.norm_rope_backward(*x[:2], wq, wk, first + i, *x[2:])[:2])
+            assert all(torch.equal(u, one(v, i)) for u, v in zip(got, both))
+    assert int(a.status.item()) == 0
