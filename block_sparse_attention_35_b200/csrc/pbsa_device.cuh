@@ -79,7 +79,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     }
 }
 
-// mbar_wait of a whole warp, with one verdict for all lanes: they look at the clock and the abort
+// mbar_wait of a whole warp, with one answer for all lanes: they look at the clock and the abort
 // flag one by one, so where one gives up another may still see the phase complete, and what
 // follows (shuffles, votes, matrix instructions of the full warp) needs all of them or none.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,

@@ -54,6 +54,7 @@ class TokenCache:
         self._count = torch.arange(capacity, **i32)
         self._turn = torch.arange(capacity, device=dev) - capacity
         self._steps = {}                        # by T: see _buffers
+        self._most = 0   # rows in use, at most; None: a replayed step adds to them unseen
 
     def _buffers(self, T: int):
         """The tensors of a step of T tokens, allocated on its first use; the least recently used
@@ -76,7 +77,8 @@ class TokenCache:
                 lse=torch.empty(self.B, self.Hq, T, dtype=torch.float32, device=dev),
                 ws=torch.empty(P.pbsa_kv4_workspace_size(self.cfg, T), dtype=torch.uint8,
                                device=dev))
-        s["captured"] |= capturing
+        if capturing:
+            s["captured"], self._most = True, None
         self._steps[T] = s   # the last: in order of use
         return s
 
@@ -105,12 +107,14 @@ class TokenCache:
         P.pbsa_kv4_evict(self.cfg, self.pos, self.mass, self.n_sink, self.seen - self.n_recent,
                          s["rows"], self.status)
         rows = s["rows"]
-        if n_new is not None and T > 1:
-            # Empty rows first.  The rows in use are the first kv_len, so that of the T chosen ones,
+        if n_new is not None and T > 1 and (self._most is None or self._most + T > self.capacity):
+            # Empty rows first, where rows in use may be among the chosen.  The rows in use are the first kv_len, so that of the T chosen ones,
             # in row order, the last capacity - kv_len are empty: they are turned to the front.
             turn = (self._turn[:T] + self.kv_len.clamp(min=self.capacity - T)[:, None]) % T
             rows = rows.gather(2, turn[:, None].expand(rows.shape))
         P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, rows, self.mass, self.status)
+        if self._most is not None:
+            self._most = min(self._most + T, self.capacity)
         self.seen += n
         torch.clamp(self.seen, max=self.capacity, out=self.kv_len)
         P.pbsa_kv4_attn(self.cfg, self.cache, q, pos, self.kv_len, s["out"], s["lse"], self.mass,

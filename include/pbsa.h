@@ -520,7 +520,7 @@ PBSA_API int pbsa_kv4_evict(const pbsa_kv4_config* cfg, const int32_t* pos, cons
  * Diagnostic: runs one kernel that waits, with the library's bounded wait, on a barrier
  * that nothing completes.  After `timeout_ns` nanoseconds the wait gives up and writes
  * PBSA_ERR_TIMEOUT into *status.  A whole warp waits as well, on a barrier that completes after
- * its first lane has given up: had its lanes not agreed on one verdict, *status would be
+ * its first lane has given up: had its lanes not agreed on one answer, *status would be
  * PBSA_ERR_DEVICE_CHECK.  The pages have no counterpart; it exists so that the timeout path can
  * be tested without hanging a GPU.
  */

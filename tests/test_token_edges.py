@@ -18,7 +18,7 @@ CSRC = os.path.join(ROOT, "block_sparse_attention_35_b200", "csrc")
 @pytest.mark.parametrize("name", ["kv4_attn.cu", "kv4_chunk.cu"])
 def test_warps_agree_on_what_a_wait_returned(name):
     """Where a whole warp waits and goes on with shuffles, votes or matrix instructions, its lanes
-    share one verdict: nothing stores a single lane's."""
+    share one answer: nothing stores a single lane's."""
     src = open(os.path.join(CSRC, name)).read()
     assert len(re.findall(r"\bmbar_wait_warp\(", src)) >= 1
     assert not re.findall(r"\bok\w*\s*=[^;]*\bmbar_wait\(", src)
