@@ -166,8 +166,8 @@ class SparseForcingAttention:
         """RMS-normalises every head of the projected queries and keys [B, frames*T_f, H, D]
         (views of one projection's output will do), scales it by its weight ([D] fp32 or None)
         and rotates it by its token's frame (first_frame, first_frame + 1, ... of the sequence,
-        below max_seq_len / T_f), row and column.  Returns new (q, k), ready for append() and
-        the call."""
+        below max_seq_len / T_f; past its table it is refused), row and column.  Returns new
+        (q, k), ready for append() and the call."""
         cfg, pos = self._heads_of(q.shape[1], first_frame, torch.bfloat16)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)

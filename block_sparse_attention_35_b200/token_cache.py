@@ -12,9 +12,10 @@ Until the cache is full the new tokens take empty rows; then a step of T tokens 
 that drew the least attention so far, sparing the sequence's first ``n_sink`` and its last
 ``n_recent`` tokens.  A padded sequence, with fewer tokens than T, takes what is empty first and
 then the first of those T rows in the order of the cache, not the lightest of them.
-Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph.  A step's output is a buffer that the next step of the same T
-writes again.  The buffers of the last ``_KEEP`` lengths are kept for the next step of their
-length, and those of a captured step as long as the cache."""
+Nothing in a step waits for the GPU, and a step can be captured into a CUDA graph.  A step's output
+is a buffer that the next step of the same T writes again.  The buffers of the last ``_KEEP``
+lengths are kept for the next step of their length, and those of a captured step as long as the
+cache."""
 from __future__ import annotations
 
 import torch
@@ -108,8 +109,9 @@ class TokenCache:
                          s["rows"], self.status)
         rows = s["rows"]
         if n_new is not None and T > 1 and (self._most is None or self._most + T > self.capacity):
-            # Empty rows first, where rows in use may be among the chosen.  The rows in use are the first kv_len, so that of the T chosen ones,
-            # in row order, the last capacity - kv_len are empty: they are turned to the front.
+            # Empty rows first, where rows in use may be among the chosen.  Those in use are the
+            # first kv_len, so that of the T chosen ones, in row order, the last capacity - kv_len
+            # are empty: they are turned to the front.
             turn = (self._turn[:T] + self.kv_len.clamp(min=self.capacity - T)[:, None]) % T
             rows = rows.gather(2, turn[:, None].expand(rows.shape))
         P.pbsa_kv4_append(self.cfg, self.cache, k, v, pos, rows, self.mass, self.status)
